@@ -457,6 +457,87 @@ QOQ_API int qoq_kv4_decode_attention(const void* Q, const uint8_t* k_codes, cons
                                      void* stream);
 
 /* ------------------------------------------------------------------------
+ * Paged 4-bit KV cache, for serving many sequences of any length: the cache
+ * vectors, codes and scales of the 4-bit KV cache above ("W4A8KV4", abstract;
+ * Insight: the fused, memory-bound attention), with every sequence's tokens in
+ * pages of a shared pool.  The pages of the sources fix no paging; this
+ * library's:
+ *   pool    k_codes, v_codes [pages][Hkv][page / 16][1024] bytes and scales
+ *           [pages][Hkv][page][4] FP16 (s_K, m_K, s_V, m_V), sizes from
+ *           qoq_kv4_paged_bytes; blocks of 16 tokens in the nibble orders given
+ *           above.  `page` (tokens a page) is a multiple of 16, d = 128.
+ *   table   block_table, int32 [B][width]: token t of sequence b lies in page
+ *           block_table[b][t / page], slot t % page.  A number outside
+ *           [0, pages) stands for no page: nothing is read or written there, and
+ *           attention leaves its tokens out.  Entries past a sequence's length
+ *           are not read.
+ *   batch   rows of T query tokens.  Sequence b has the rows q_start[b] ..
+ *           q_start[b + 1] - 1 (int32 [B + 1], non-decreasing, in [0, T]; equal
+ *           for a sequence without rows); they are the last tokens of the
+ *           seqlen[b] (int32) tokens that it has with them: the i-th of n has
+ *           position seqlen[b] - n + i.  Rows before q_start[0] and behind
+ *           q_start[B] belong to no sequence and their outputs are left as they
+ *           were (padded batches).  All of these are device arrays, read by the
+ *           kernels: a captured graph follows their contents.
+ *   limits  width * page < 2^31 tokens, pages * Hkv * page / 16 < 2^31 blocks,
+ *           Hq, Hkv <= 65535 (QOQ_ERR_UNSUPPORTED past them).
+ * T = 0 and B = 0 are calls with nothing to do.
+ * ---------------------------------------------------------------------- */
+QOQ_API int qoq_kv4_paged_bytes(int pages, int Hkv, int page, int d, size_t* k_bytes,
+                                size_t* v_bytes, size_t* scale_bytes);
+
+/* Rotate and append: the T rows of a fused QKV projection, qkv [T][Hq + 2 Hkv]
+ * [128] FP16 with `ld` elements between rows (ld >= (Hq + 2 Hkv) * 128, a
+ * multiple of 8), query heads first, then keys, then values.
+ *   rotation  Queries and keys turn their first `rot` dimensions (a multiple of
+ *             16, 0 .. 128; the rest passes) by position * inv_freq[j] radians
+ *             (device, binary64 [rot / 2]: any scaling for long contexts is in
+ *             it); pair j is the dimensions j and j + rot / 2, or 2j and 2j + 1
+ *             with interleaved = 1; rotated values are multiplied by
+ *             rope_factor.  rot = 0 (inv_freq may be NULL): no rotation.
+ *   q_out     [T][Hq][128] FP16, written: the rotated queries.  Not the memory
+ *             of qkv.
+ *   cache     Keys, rotated in binary64 and rounded to binary32 and then FP16,
+ *             and values are quantized as by qoq_kv4_quantize and written to
+ *             their slots.  A position outside [0, width * page) or in no page is
+ *             not written.  Only the token's own codes change in the words it
+ *             shares; sequences may append to one page in one call.  A slot that
+ *             two rows of one call name holds unspecified codes afterwards.
+ *   k_values, v_values  [T][Hkv][128] FP16, written, or both NULL: the values
+ *             fp16(s q + m) that the cache then stands for (for attention in
+ *             FP16 over what later steps will read).
+ * Asynchronous on `stream`. */
+QOQ_API int qoq_kv4_paged_append(const void* qkv, size_t ld, int T, int Hq, int Hkv, int d,
+                                 const int* q_start, const int* seqlen, int B,
+                                 const int* block_table, int width, int pages, int page,
+                                 const double* inv_freq, int rot, int interleaved,
+                                 double rope_factor, void* q_out, uint8_t* k_codes,
+                                 uint8_t* v_codes, void* scales, void* k_values, void* v_values,
+                                 void* stream);
+
+/* Causal attention of the T query rows over the paged cache:
+ *   out[r][h] = softmax_t(scale * Q[r][h] . k^[t]) . v^[t]   over the tokens
+ * t <= position of r, t < min(seqlen, width * page), of the row's sequence, KV
+ * head h / (Hq / Hkv), Hq % Hkv == 0.  A row that sees no token gives 0.
+ * Q [T][Hq][128] FP16 with ldq elements between rows (ldq >= Hq * 128, a
+ * multiple of 8); out [T][Hq][128] FP16.  max_q: the largest number of query
+ * tokens of a sequence (1 for a decode step; T is always safe): it picks the
+ * kernels, and a sequence with more is left as it was.  ws: at least
+ * qoq_kv4_paged_attention_workspace_bytes for the same arguments, 16-byte
+ * aligned (no zeroing needed), QOQ_ERR_WORKSPACE otherwise; calls that can run
+ * at the same time need different workspaces.  Scores, softmax statistics and
+ * sums are FP32.  Results do not depend on what else runs.  Asynchronous on
+ * `stream`. */
+QOQ_API size_t qoq_kv4_paged_attention_workspace_bytes(int T, int Hq, int Hkv, int d, int B,
+                                                       int width, int page, int max_q);
+QOQ_API int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq, int Hkv, int d,
+                                    const uint8_t* k_codes, const uint8_t* v_codes,
+                                    const void* scales, const int* q_start, const int* seqlen,
+                                    int B, const int* block_table, int width, int pages, int page,
+                                    int max_q, float scale, void* out, void* ws, size_t ws_bytes,
+                                    void* stream);
+
+/* ------------------------------------------------------------------------
  * Device-side error word.  Every wait inside the kernels is bounded; a wait
  * that runs out sets a bit in this word and the kernel returns early
  * instead of hanging.  Synchronous (device-wide): reads the word of the

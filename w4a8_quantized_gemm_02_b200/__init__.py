@@ -37,6 +37,8 @@ EXPORTS = (
     "qoq_quantize_weights_gate_up", "qoq_w4a8_gate_up_silu",
     "qoq_kv4_cache_bytes", "qoq_kv4_quantize", "qoq_kv4_attention_workspace_bytes",
     "qoq_kv4_decode_attention",
+    "qoq_kv4_paged_bytes", "qoq_kv4_paged_append", "qoq_kv4_paged_attention_workspace_bytes",
+    "qoq_kv4_paged_attention",
 )
 
 _lock = threading.Lock()
@@ -117,6 +119,16 @@ def lib() -> ctypes.CDLL:
             L.qoq_kv4_attention_workspace_bytes.argtypes = [I, I, I, I, I]
             L.qoq_kv4_decode_attention.restype = I
             L.qoq_kv4_decode_attention.argtypes = [P, P, P, P, P, I, I, I, I, I, P, P, sz, P]
+            L.qoq_kv4_paged_bytes.restype = I
+            L.qoq_kv4_paged_bytes.argtypes = [I, I, I, I] + [ctypes.POINTER(sz)] * 3
+            L.qoq_kv4_paged_append.restype = I
+            L.qoq_kv4_paged_append.argtypes = ([P, sz, I, I, I, I, P, P, I, P, I, I, I, P, I, I,
+                                                ctypes.c_double] + [P] * 7)
+            L.qoq_kv4_paged_attention_workspace_bytes.restype = sz
+            L.qoq_kv4_paged_attention_workspace_bytes.argtypes = [I] * 8
+            L.qoq_kv4_paged_attention.restype = I
+            L.qoq_kv4_paged_attention.argtypes = [P, sz, I, I, I, I, P, P, P, P, P, I, P, I, I, I,
+                                                  I, ctypes.c_float, P, P, sz, P]
             L.qoq_device_error.restype = I
             L.qoq_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), I]
             _lib = L
@@ -445,6 +457,244 @@ def kv4_decode_attention(Q, cache, seqlen, out=None, ws=None, stream=None):
                                           ws.numel() * ws.element_size(), _stream(stream)),
            "qoq_kv4_decode_attention")
     return out
+
+
+# ---------------------------------------------------------------------------
+# paged 4-bit KV cache
+# ---------------------------------------------------------------------------
+
+class _on:
+    """The device of `t` as the current one, and the stream of a call on it:
+    the caller's, or the device's current stream.  Outputs and workspaces are
+    allocated inside, so they belong to that stream."""
+
+    def __init__(self, t, stream):
+        import torch
+        if stream is not None and stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+        self._device = torch.cuda.device(t.device)
+        self._stream = torch.cuda.stream(stream)
+
+    def __enter__(self):
+        self._device.__enter__()
+        self._stream.__enter__()
+        return _stream()
+
+    def __exit__(self, *exc):
+        self._stream.__exit__(*exc)
+        self._device.__exit__(*exc)
+
+
+def _need_rows(t, name, dtype, width, device=None):
+    """A CUDA tensor of rows of `width` contiguous elements, the rows any
+    multiple of 16 bytes apart; returns (rows, elements between rows)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    rows, at = t.shape[0], 1
+    for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if size != 1 and step != at:
+            raise ValueError(f"{name}: the elements of a row must be contiguous")
+        at *= size
+    if at != width:
+        raise ValueError(f"{name} must have rows of {width} elements, got {at}")
+    ld = t.stride(0) if rows > 1 else width
+    if ld < width or ld * t.element_size() % 16:
+        raise ValueError(f"{name}: rows must be {width} or more elements and a multiple of 16 "
+                         f"bytes apart, got {ld}")
+    return rows, ld
+
+
+def _need_batch(cache, q_start, seqlen, block_table, device):
+    """Checks a paged cache and a ragged batch; returns (pages, Hkv, page, B, width)."""
+    import torch
+    kc, vc, sc = cache
+    _need_cuda(sc, "scales", torch.float16, 4, device=device)
+    pages, Hkv, page, four = sc.shape
+    if four != 4 or page % 16:
+        raise ValueError("scales must have shape (pages, Hkv, page, 4), page a multiple of 16")
+    shape = (pages, Hkv, page // 16, 1024)
+    _need_cuda(kc, "k_codes", torch.uint8, shape=shape, device=device)
+    _need_cuda(vc, "v_codes", torch.uint8, shape=shape, device=device)
+    _need_cuda(seqlen, "seqlen", torch.int32, 1, device=device)
+    B = seqlen.shape[0]
+    _need_cuda(q_start, "q_start", torch.int32, shape=(B + 1,), device=device)
+    _need_cuda(block_table, "block_table", torch.int32, 2, device=device)
+    if block_table.shape[0] != B:
+        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
+    return pages, Hkv, page, B, block_table.shape[1]
+
+
+def kv4_paged_bytes(pages: int, Hkv: int, page: int, d: int = 128):
+    """(k_bytes, v_bytes, scale_bytes) of a paged 4-bit KV cache."""
+    k, v, sc = ctypes.c_size_t(), ctypes.c_size_t(), ctypes.c_size_t()
+    _check(lib().qoq_kv4_paged_bytes(pages, Hkv, page, d, ctypes.byref(k), ctypes.byref(v),
+                                     ctypes.byref(sc)), "qoq_kv4_paged_bytes")
+    return k.value, v.value, sc.value
+
+
+def kv4_paged_cache(pages: int, Hkv: int, page: int, device, d: int = 128):
+    """An empty pool of `pages` pages of `page` tokens: (k_codes uint8, v_codes
+    uint8, scales float16), (pages, Hkv, page // 16, 1024) twice and
+    (pages, Hkv, page, 4)."""
+    import torch
+    kv4_paged_bytes(pages, Hkv, page, d)
+    kc = torch.zeros((pages, Hkv, page // 16, 1024), dtype=torch.uint8, device=device)
+    vc = torch.zeros((pages, Hkv, page // 16, 1024), dtype=torch.uint8, device=device)
+    sc = torch.zeros((pages, Hkv, page, 4), dtype=torch.float16, device=device)
+    return kc, vc, sc
+
+
+def rope_frequencies(rot: int = 128, base: float = 10000.0, scaling=None, device="cuda"):
+    """(inv_freq, factor) of a rotary embedding over `rot` dimensions: the
+    radians per position of its rot / 2 pairs as a float64 tensor, and the
+    factor on rotated values, for kv4_paged_append.
+
+    scaling: None, or a dict with "type" and the type's numbers, for contexts
+    longer than the trained one:
+      "linear"  factor: positions divided by it
+      "ntk"     factor: base * factor ** (rot / (rot - 2))
+      "llama3"  factor, low_freq_factor, high_freq_factor, original_length:
+                wavelengths over original_length / low_freq_factor are divided,
+                those under original_length / high_freq_factor kept, those
+                between interpolated
+      "yarn"    factor, original_length, beta_fast (32), beta_slow (1),
+                attention_factor (0.1 ln factor + 1): pairs that turn less than
+                beta_slow times over the trained length divided, more than
+                beta_fast times kept, a ramp between."""
+    import math
+
+    import torch
+    if rot <= 0 or rot > 128 or rot % 16:
+        raise ValueError("rot must be a multiple of 16 in 16 .. 128")
+    if not base > 1.0:
+        raise ValueError("base must be over 1")
+    scaling = dict(scaling or {"type": "none"})
+    kind = scaling.pop("type", None)
+    allowed = {"none": (), "linear": ("factor",), "ntk": ("factor",),
+               "llama3": ("factor", "low_freq_factor", "high_freq_factor", "original_length"),
+               "yarn": ("factor", "original_length", "beta_fast", "beta_slow",
+                        "attention_factor")}
+    if kind not in allowed:
+        raise ValueError(f"unknown scaling type {kind!r}")
+    if set(scaling) - set(allowed[kind]):
+        raise ValueError(f"{kind} scaling takes {allowed[kind]}, got {sorted(scaling)}")
+    missing = set(allowed[kind]) - set(scaling) - {"beta_fast", "beta_slow", "attention_factor"}
+    if missing:
+        raise ValueError(f"{kind} scaling needs {sorted(missing)}")
+    factor = float(scaling.get("factor", 1.0))
+    if not factor > 0.0:
+        raise ValueError("factor must be positive")
+    if kind == "ntk":
+        base = base * factor ** (rot / (rot - 2))
+    freq = [base ** (-2.0 * j / rot) for j in range(rot // 2)]
+    attention = 1.0
+    if kind == "linear":
+        freq = [f / factor for f in freq]
+    elif kind == "llama3":
+        length = float(scaling["original_length"])
+        low, high = float(scaling["low_freq_factor"]), float(scaling["high_freq_factor"])
+        if not high > low:
+            raise ValueError("high_freq_factor must be over low_freq_factor")
+        turns = [length * f / (2.0 * math.pi) for f in freq]
+        keep = [min(1.0, max(0.0, (t - low) / (high - low))) for t in turns]
+        freq = [(1.0 - k) * f / factor + k * f for f, k in zip(freq, keep)]
+    elif kind == "yarn":
+        length = float(scaling["original_length"])
+        fast, slow = float(scaling.get("beta_fast", 32.0)), float(scaling.get("beta_slow", 1.0))
+
+        def pair_of(turns):   # the pair that turns so often over the trained length
+            return rot * math.log(length / (turns * 2.0 * math.pi)) / (2.0 * math.log(base))
+        lo, hi = max(0, math.floor(pair_of(fast))), min(rot - 1, math.ceil(pair_of(slow)))
+        ramp = [min(1.0, max(0.0, (j - lo) / max(hi - lo, 1e-3))) for j in range(rot // 2)]
+        freq = [f / factor * r + f * (1.0 - r) for f, r in zip(freq, ramp)]
+        attention = float(scaling.get("attention_factor", 0.1 * math.log(factor) + 1.0
+                                      if factor > 1.0 else 1.0))
+    return torch.tensor(freq, dtype=torch.float64, device=device), attention
+
+
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+
+
+def kv4_paged_append(qkv, cache, q_start, seqlen, block_table, Hq: int, inv_freq=None,
+                     rope_layout: str = "half", rope_factor: float = 1.0, q_out=None, values=None,
+                     stream=None):
+    """Rotate the queries and keys of qkv ((T, (Hq + 2 Hkv) * 128) float16, rows
+    may be strided) to their positions, quantize keys and values into their
+    pages, and return the queries, (T, Hq, 128) float16.
+
+    q_start (B + 1) and seqlen (B), int32: sequence b has the rows q_start[b] ..
+    q_start[b + 1] - 1, its last tokens of seqlen[b]; block_table (B, width)
+    int32.  inv_freq: float64 (rot / 2) from rope_frequencies (None: no
+    rotation), rope_layout "half" or "interleaved".  values: (K, V), each
+    (T, Hkv, 128) float16, written with the values that the cache then holds."""
+    import torch
+    if rope_layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"rope_layout must be one of {sorted(_ROPE_LAYOUTS)}")
+    if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda:
+        raise ValueError("qkv must be a CUDA tensor")
+    dev = qkv.device
+    pages, Hkv, page, B, width = _need_batch(cache, q_start, seqlen, block_table, dev)
+    T, ld = _need_rows(qkv, "qkv", torch.float16, (Hq + 2 * Hkv) * 128)
+    rot = 0
+    if inv_freq is not None:
+        _need_cuda(inv_freq, "inv_freq", torch.float64, 1, device=dev)
+        rot = 2 * inv_freq.shape[0]
+    kh, vh = values if values is not None else (None, None)
+    for t, name in ((kh, "values[0]"), (vh, "values[1]")):
+        if values is not None:
+            _need_cuda(t, name, torch.float16, shape=(T, Hkv, 128), device=dev)
+    with _on(qkv, stream) as s:
+        q_out = _out(q_out, (T, Hq, 128), torch.float16, dev)
+        _check(lib().qoq_kv4_paged_append(
+            _ptr(qkv), ld, T, Hq, Hkv, 128, _ptr(q_start), _ptr(seqlen), B, _ptr(block_table),
+            width, pages, page, _ptr(inv_freq), rot, _ROPE_LAYOUTS[rope_layout],
+            float(rope_factor), _ptr(q_out), _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]),
+            _ptr(kh), _ptr(vh), s), "qoq_kv4_paged_append")
+    return q_out
+
+
+def kv4_paged_attention(Q, cache, q_start, seqlen, block_table, max_q=None, scale=None, out=None,
+                        ws=None, stream=None):
+    """Causal attention of the rows of Q ((T, Hq, 128) float16, rows may be
+    strided) over the paged cache; returns (T, Hq, 128) float16.
+
+    The batch as for kv4_paged_append, after the append.  max_q: the largest
+    number of rows of a sequence (1 for a decode step; default: T).  scale:
+    default 1 / sqrt(128).  ws: a uint8 workspace of
+    kv4_paged_attention_workspace_bytes (default: allocated for the call)."""
+    import math
+
+    import torch
+    if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.shape[2] != 128:
+        raise ValueError("Q must have shape (T, Hq, 128)")
+    Hq, dev = Q.shape[1], Q.device
+    T, ldq = _need_rows(Q, "Q", torch.float16, Hq * 128)
+    pages, Hkv, page, B, width = _need_batch(cache, q_start, seqlen, block_table, dev)
+    max_q = max(T, 1) if max_q is None else int(max_q)
+    scale = 1.0 / math.sqrt(128.0) if scale is None else float(scale)
+    _need_ws(ws, dev)
+    with _on(Q, stream) as s:
+        out = _out(out, (T, Hq, 128), torch.float16, dev)
+        if ws is None:
+            need = kv4_paged_attention_workspace_bytes(T, Hq, Hkv, B, width, page, max_q)
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+        w, wb = _ws_args(ws)
+        _check(lib().qoq_kv4_paged_attention(
+            _ptr(Q), ldq, T, Hq, Hkv, 128, _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]),
+            _ptr(q_start), _ptr(seqlen), B, _ptr(block_table), width, pages, page, max_q, scale,
+            _ptr(out), w, wb, s), "qoq_kv4_paged_attention")
+    return out
+
+
+def kv4_paged_attention_workspace_bytes(T: int, Hq: int, Hkv: int, B: int, width: int, page: int,
+                                        max_q: int) -> int:
+    return int(lib().qoq_kv4_paged_attention_workspace_bytes(T, Hq, Hkv, 128, B, width, page,
+                                                             max_q))
 
 
 def smooth_factors(Xcal, W, stream=None):

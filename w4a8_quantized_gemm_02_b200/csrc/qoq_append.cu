@@ -1,0 +1,296 @@
+// Appending the rows of a fused QKV projection to a paged 4-bit KV cache, with
+// the position rotation (RoPE) applied on the way.
+//
+// Row r, the i-th of the n query tokens of its sequence, has position
+// p = seqlen - n + i.  The pairs of the rotated part of every query and key
+// head turn by p * inv_freq[j] radians:
+//     (x0, x1) -> factor * (x0 cos - x1 sin, x1 cos + x0 sin),
+// pair j being the dimensions (j, j + rot/2) or (2j, 2j + 1).  Queries are
+// rounded to FP16 and returned; keys are rounded to binary32 and then FP16, and
+// keys and values quantized per (token, head) vector as kv4_quantize does.
+//
+// Precision.  A key beside a code's border moves by a whole step (1/15 of its
+// vector's range) if its rotation is off in the last bit, so angles and keys
+// are rotated in binary64.  The angle is reduced in turns: with 1/(2 pi) as a
+// pair of doubles, h + l = inv_freq / (2 pi) to about 2^-100, p h is split by an
+// FMA into its rounded value and the rest, and the fraction of a turn goes to
+// sincospi: the error is about 2^-53 turns for any 32-bit position.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "qoq.h"
+#include "qoq_device.cuh"
+#include "qoq_internal.h"
+#include "qoq_kv4.cuh"
+#include "qoq_paged.h"
+
+namespace qoq {
+namespace {
+
+struct AppendArgs {
+  const __half* qkv;
+  size_t ld;                  // elements between rows
+  int T, Hq, Hkv, B;
+  const int* q_start;
+  const int* seqlen;
+  const int* table;
+  int width, pages, page;
+  const double* inv_freq;     // rot / 2 of them
+  int rot;                    // rotated dimensions of a head (0: none)
+  int interleaved;
+  double factor;
+  __half* q_out;
+  uint8_t* kc;
+  uint8_t* vc;
+  __half* sc;
+  __half* k_hat;              // optional: the values the cache then holds
+  __half* v_hat;
+};
+
+// factor * (cos, sin) of p * f radians.
+__device__ __forceinline__ double2 rope_cos_sin(long long p, double f, double factor) {
+  const double kInvTau = 0.15915494309189535, kInvTauLow = -9.839338337591243e-18;
+  const double h = f * kInvTau;
+  const double l = fma(f, kInvTau, -h) + f * kInvTauLow;
+  const double pd = static_cast<double>(p);
+  const double t = pd * h;
+  const double r = (t - rint(t)) + (fma(pd, h, -t) + pd * l);   // the fraction of a turn
+  double s, c;
+  sincospi(2.0 * r, &s, &c);
+  return make_double2(c * factor, s * factor);
+}
+
+__device__ __forceinline__ void load8(const __half* p, __half (&x)[8]) {
+  *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void store8(__half* p, const __half (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = *reinterpret_cast<const uint4*>(x);
+}
+
+// Scale, offset and codes of a vector of 128 spread over 8 lanes, 16 values a
+// lane: the arithmetic of kv4_params / kv4_code.
+__device__ __forceinline__ Quant4 kv4_params16(const float (&x)[16]) {
+  float mn = x[0], mx = x[0];
+#pragma unroll
+  for (int u = 1; u < 16; ++u) {
+    mn = fminf(mn, x[u]);
+    mx = fmaxf(mx, x[u]);
+  }
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  }
+  Quant4 r;
+  r.s = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
+  r.sf = __half2float(r.s);
+  r.mn = mn;
+  r.m = mn == 0.0f ? __float2half_rn(0.0f) : __float2half_rn(mn);
+  return r;
+}
+
+// Replace the nibbles under `mask` of *word by those of `bits`.  The exclusive
+// or changes no other nibble, so tokens of one word may be written at the same
+// time by different threads.
+__device__ __forceinline__ void put_nibbles(uint32_t* word, uint32_t bits, uint32_t mask) {
+  const uint32_t diff = (*word ^ bits) & mask;
+  if (diff) atomicXor(word, diff);
+}
+
+// Grid (T, ceil((Hq + 2 Hkv) / 32)), 256 threads.  Eight lanes take one vector
+// (a query, key or value head of the row), lane i its dimensions 16i .. 16i+15,
+// which are word i of the runs that hold the token.
+__global__ void __launch_bounds__(256) append_rows_kernel(const AppendArgs a) {
+  __shared__ double2 cs[kHeadDim / 2];
+  const int row = blockIdx.x, tid = threadIdx.x;
+  const int vec = blockIdx.y * 32 + (tid >> 3), i = tid & 7;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  // the sequence of the row: the last one that starts at or before it
+  int b = -1;
+  for (int at = 0; at < a.B; at += 256) {
+    const int c = at + tid;
+    b += __syncthreads_count(c < a.B && a.q_start[c < a.B ? c : 0] <= row);
+  }
+  if (b < 0) return;
+  const RowRange rr = rows_of(a.q_start, b, a.T);
+  if (row < rr.first || row >= rr.first + rr.n) return;   // behind the last sequence
+  const long long pos = position_of(a.seqlen[b], rr.n, row - rr.first);
+  if (tid < (a.rot >> 1)) cs[tid] = rope_cos_sin(pos, a.inv_freq[tid], a.factor);
+  __syncthreads();
+
+  const int heads = a.Hq + 2 * a.Hkv;
+  const bool mine = vec < heads;
+  const __half* src = a.qkv + static_cast<size_t>(row) * a.ld + static_cast<size_t>(vec) * kHeadDim;
+  __half x[2][8];
+  if (mine) {
+    load8(src + 16 * i, x[0]);
+    load8(src + 16 * i + 8, x[1]);
+  } else {
+#pragma unroll
+    for (int u = 0; u < 16; ++u) x[u >> 3][u & 7] = __float2half_rn(0.0f);
+  }
+  if (mine && vec < a.Hq + a.Hkv) {
+    const int half_rot = a.rot >> 1;
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const int d0 = 16 * i + 8 * q;
+      if (d0 >= a.rot) continue;
+      if (a.interleaved) {
+#pragma unroll
+        for (int u = 0; u < 8; u += 2) {
+          const double2 w = cs[(d0 + u) >> 1];
+          const double x0 = __half2float(x[q][u]), x1 = __half2float(x[q][u + 1]);
+          x[q][u] = __float2half_rn(static_cast<float>(x0 * w.x - x1 * w.y));
+          x[q][u + 1] = __float2half_rn(static_cast<float>(x1 * w.x + x0 * w.y));
+        }
+      } else {
+        const bool low = d0 < half_rot;
+        __half o[8];
+        load8(src + (low ? d0 + half_rot : d0 - half_rot), o);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const double2 w = cs[(low ? d0 : d0 - half_rot) + u];
+          const double xs = __half2float(x[q][u]), os = __half2float(o[u]);
+          x[q][u] = __float2half_rn(static_cast<float>(xs * w.x + (low ? -os : os) * w.y));
+        }
+      }
+    }
+  }
+  if (mine && vec < a.Hq) {
+    __half* dst = a.q_out + (static_cast<size_t>(row) * a.Hq + vec) * kHeadDim + 16 * i;
+    store8(dst, x[0]);
+    store8(dst + 8, x[1]);
+  }
+  // keys and values (the shuffles need whole warps: eight-lane groups without a
+  // vector quantize zeros)
+  if (blockIdx.y * 32 + 32 <= a.Hq) return;
+  float f[16];
+#pragma unroll
+  for (int u = 0; u < 16; ++u) f[u] = __half2float(x[u >> 3][u & 7]);
+  const Quant4 p = kv4_params16(f);
+  if (!mine || vec < a.Hq) return;
+  const bool is_v = vec >= a.Hq + a.Hkv;
+  const int hk = vec - a.Hq - (is_v ? a.Hkv : 0);
+  int code[16];
+#pragma unroll
+  for (int u = 0; u < 16; ++u) code[u] = kv4_code(f[u], p);
+  __half* hat = is_v ? a.v_hat : a.k_hat;
+  if (hat) {
+    const float m = __half2float(p.m);
+    hat += (static_cast<size_t>(row) * a.Hkv + hk) * kHeadDim + 16 * i;
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+      x[u >> 3][u & 7] = __float2half_rn(fmaf(static_cast<float>(code[u]), p.sf, m));
+    store8(hat, x[0]);
+    store8(hat + 8, x[1]);
+  }
+  const int ppb = a.page >> 4;
+  if (pos < 0 || pos >= static_cast<long long>(a.width) * a.page) return;   // no slot
+  const int blk = pool_block(a.table + static_cast<size_t>(b) * a.width, static_cast<int>(pos >> 4),
+                             ppb, a.pages, a.Hkv, hk);
+  if (blk < 0) return;
+  const int t = static_cast<int>(pos & 15);
+  if (i == 0)
+    *reinterpret_cast<__half2*>(a.sc + static_cast<size_t>(blk) * 64 + 4 * t + (is_v ? 2 : 0)) =
+        __halves2half2(p.s, p.m);
+  if (!is_v) {
+    // token t: gid = t & 7, nibbles j0 = t >> 3; dimension 16 i + 2 tig + e + 8 j1
+    uint32_t* w = reinterpret_cast<uint32_t*>(a.kc + static_cast<size_t>(blk) * 1024) +
+                  (t & 7) * 32 + i;
+    const int sh = (t >> 3) * 4;
+#pragma unroll
+    for (int tig = 0; tig < 4; ++tig) {
+      uint32_t bits = 0;
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j1 = 0; j1 < 2; ++j1)
+          bits |= static_cast<uint32_t>(code[2 * tig + e + 8 * j1]) << (16 * e + 8 * j1);
+      put_nibbles(w + tig * 8, bits << sh, 0x0f0f0f0fu << sh);
+    }
+  } else {
+    // token t: tig = (t & 7) >> 1, e = t & 1, j1 = t >> 3; dimension
+    // 16 i + gid + 8 j0
+    uint32_t* w = reinterpret_cast<uint32_t*>(a.vc + static_cast<size_t>(blk) * 1024) +
+                  ((t & 7) >> 1) * 8 + i;
+    const int sh = 16 * (t & 1) + 8 * (t >> 3);
+#pragma unroll
+    for (int gid = 0; gid < 8; ++gid) {
+      const uint32_t bits = static_cast<uint32_t>(code[gid] | (code[gid + 8] << 4));
+      put_nibbles(w + gid * 32, bits << sh, 0xffu << sh);
+    }
+  }
+}
+
+}  // namespace
+
+int check_paged_shape(int pages, int Hkv, int page, int d) {
+  if (pages <= 0 || Hkv <= 0 || page <= 0) return QOQ_ERR_INVALID_ARG;
+  if (d != kHeadDim || page % 16 != 0) return QOQ_ERR_UNSUPPORTED;
+  if (Hkv > 65535) return QOQ_ERR_UNSUPPORTED;
+  // block numbers of 16 tokens are 32-bit
+  if (static_cast<long long>(Hkv) * (page / 16) > 0x7fffffffLL / pages) return QOQ_ERR_UNSUPPORTED;
+  return QOQ_OK;
+}
+
+int check_batch(int T, int B, int width, int page) {
+  if (T < 0 || B < 0 || width <= 0) return QOQ_ERR_INVALID_ARG;
+  if (width > 0x7fffffff / page) return QOQ_ERR_UNSUPPORTED;   // positions are 32-bit
+  return QOQ_OK;
+}
+
+}  // namespace qoq
+
+using namespace qoq;
+
+extern "C" int qoq_kv4_paged_bytes(int pages, int Hkv, int page, int d, size_t* k_bytes,
+                                   size_t* v_bytes, size_t* scale_bytes) {
+  if (int st = check_paged_shape(pages, Hkv, page, d)) return st;
+  const size_t blocks = static_cast<size_t>(pages) * Hkv * (page / 16);
+  if (k_bytes) *k_bytes = blocks * 1024;
+  if (v_bytes) *v_bytes = blocks * 1024;
+  if (scale_bytes) *scale_bytes = blocks * 128;
+  return QOQ_OK;
+}
+
+extern "C" int qoq_kv4_paged_append(const void* qkv, size_t ld, int T, int Hq, int Hkv, int d,
+                                    const int* q_start, const int* seqlen, int B,
+                                    const int* block_table, int width, int pages, int page,
+                                    const double* inv_freq, int rot, int interleaved,
+                                    double rope_factor, void* q_out, uint8_t* k_codes,
+                                    uint8_t* v_codes, void* scales, void* k_values,
+                                    void* v_values, void* stream) {
+  if (Hq <= 0) return QOQ_ERR_INVALID_ARG;
+  if (int st = check_paged_shape(pages, Hkv, page, d)) return st;
+  if (int st = check_batch(T, B, width, page)) return st;
+  if (Hq > 65535) return QOQ_ERR_UNSUPPORTED;
+  if (rot < 0 || rot > kHeadDim || (rot > 0 && !inv_freq)) return QOQ_ERR_INVALID_ARG;
+  if (rot % 16 != 0) return QOQ_ERR_UNSUPPORTED;
+  if (interleaved != 0 && interleaved != 1) return QOQ_ERR_INVALID_ARG;
+  if (ld < (static_cast<size_t>(Hq) + 2 * static_cast<size_t>(Hkv)) * kHeadDim || ld % 8 != 0)
+    return QOQ_ERR_INVALID_ARG;
+  if (T == 0 || B == 0) return QOQ_OK;
+  if (!qkv || !q_start || !seqlen || !block_table || !q_out || !k_codes || !v_codes || !scales)
+    return QOQ_ERR_INVALID_ARG;
+  if (!k_values != !v_values) return QOQ_ERR_INVALID_ARG;
+  if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(k_codes) || !aligned16(v_codes) ||
+      !aligned16(scales) || !aligned16(k_values) || !aligned16(v_values) ||
+      (reinterpret_cast<uintptr_t>(inv_freq) & 7u) || !aligned4(q_start) || !aligned4(seqlen) ||
+      !aligned4(block_table))
+    return QOQ_ERR_INVALID_ARG;
+  if (int st = check_device()) return st;
+  AppendArgs a;
+  a.qkv = static_cast<const __half*>(qkv);
+  a.ld = ld;
+  a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.B = B;
+  a.q_start = q_start; a.seqlen = seqlen; a.table = block_table;
+  a.width = width; a.pages = pages; a.page = page;
+  a.inv_freq = inv_freq; a.rot = rot; a.interleaved = interleaved; a.factor = rope_factor;
+  a.q_out = static_cast<__half*>(q_out);
+  a.kc = k_codes; a.vc = v_codes; a.sc = static_cast<__half*>(scales);
+  a.k_hat = static_cast<__half*>(k_values); a.v_hat = static_cast<__half*>(v_values);
+  const unsigned groups = static_cast<unsigned>((Hq + 2 * Hkv + 31) / 32);
+  return launch_dependent(append_rows_kernel, dim3(static_cast<unsigned>(T), groups), 256, 0,
+                          as_stream(stream), a);
+}

@@ -1,0 +1,55 @@
+// What the paged attention kernels share: arguments, the launch plan and the
+// output store.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "qoq_internal.h"
+
+namespace qoq {
+
+struct PagedArgs {
+  const __half* Q;          // T rows of Hq heads, ldq elements apart
+  size_t ldq;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const __half* sc;
+  const int* q_start;       // B + 1
+  const int* seqlen;        // B
+  const int* table;         // B x width page numbers
+  int T, B, Hq, Hkv, g, width, pages, page, max_q;
+  float scale;
+  __half* out;              // T x Hq x 128
+  int2* meta;               // per (sequence, KV head): first unit and splits
+  float* parts;             // per unit and row: a partial result (kPartFloats)
+};
+
+// A sequence with at most kDecodeRows<nt> rows (query tokens x g) runs in the
+// decode kernel with 8 nt columns, a longer one in the prompt kernel.
+struct PagedPlan {
+  int nt;                   // 8-column tiles of the decode kernel: 1, 2, or 0 (not launched)
+  int target;               // splits it aims at for the whole batch
+  int grid;
+  bool combine;             // a sequence may be split
+  bool prompt;              // sequences with more rows may be there
+  int tiles;                // prompt: row-tile slots of the batch
+  int prompt_target;        // prompt: splits aimed at (0: never split)
+  int prompt_grid;
+  size_t meta_off, parts_off, prompt_meta_off, prompt_parts_off, bytes;
+};
+PagedPlan paged_plan(int T, int B, int Hq, int Hkv, int width, int page, int max_q);
+
+int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, cudaStream_t s);
+
+// 8 outputs times `f`, rounded to FP16.
+__device__ __forceinline__ void store_row8(__half* dst, const float (&v)[8], float f) {
+  __half2 o[4];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) o[k] = __floats2half2_rn(v[2 * k] * f, v[2 * k + 1] * f);
+  *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(o);
+}
+
+}  // namespace qoq

@@ -20,6 +20,8 @@ inline bool aligned16(const void* p) {
   return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
 }
 
+inline bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 inline cudaStream_t as_stream(void* s) { return reinterpret_cast<cudaStream_t>(s); }
 
 inline size_t block_bytes(int group) {
@@ -43,6 +45,33 @@ int check_device();
 int sm_count();
 // cudaGetLastError -> status.
 int launch_status();
+
+// Launch `kernel` as a programmatic dependent of the kernel before it on the
+// stream: it may be scheduled while that one drains, and every CTA of it waits
+// (grid_dependency_wait) before it touches memory.
+template <typename... Params, typename... Args>
+int launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_t smem,
+                     cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kernel, args...) != cudaSuccess) {
+    cudaGetLastError();
+    return QOQ_ERR_CUDA;
+  }
+  return QOQ_OK;
+}
+
+// Checks shared by the entry points over a paged cache (qoq_append.cu).
+int check_paged_shape(int pages, int Hkv, int page, int d);
+int check_batch(int T, int B, int width, int page);
 
 // The CUDA-core GEMV for one to four tokens (qoq_gemv.cu): same integer
 // product and epilogue as the tensor-core GEMM.  Launched as a programmatic
