@@ -538,6 +538,25 @@ QOQ_API int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq, in
                                     void* stream);
 
 /* ------------------------------------------------------------------------
+ * Low-rank adapters of many requests beside a shared projection (the outputs
+ * of qoq_w4a8_linear; the pages have no counterpart):
+ *   out[t] = fp16(Y[t] + scaling[a] * B_a . (A_a . x_t)),   a = ids[t],
+ * and out[t] = Y[t] where ids[t] is outside [0, n).
+ *   X [T][K], Y, out [T][N] FP16 (out may be Y); A [n][R][K], B [n][N][R] FP16;
+ *   ids int32 [T] (any order; runs of one adapter are quicker); scaling FP32
+ *   [n].  N % 128 == 0, K % 128 == 0, R % 8 == 0, R <= 128 (adapters of smaller
+ *   rank: zeros), T <= 2^20; T = 0 is a call with nothing to do.
+ *   ws: at least qoq_lora_workspace_bytes, 16-byte aligned (no zeroing needed),
+ *   QOQ_ERR_WORKSPACE otherwise; calls that can run at the same time need
+ *   different workspaces.
+ * Both products have FP32 sums in a fixed order; A_a . x_t enters the second
+ * with 22 bits.  Asynchronous on `stream`. */
+QOQ_API size_t qoq_lora_workspace_bytes(int T, int K, int N, int R, int n);
+QOQ_API int qoq_lora_add(const void* Y, const void* X, int T, int K, int N, const void* A,
+                         const void* B, int R, int n, const int* ids, const float* scaling,
+                         void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
  * Device-side error word.  Every wait inside the kernels is bounded; a wait
  * that runs out sets a bit in this word and the kernel returns early
  * instead of hanging.  Synchronous (device-wide): reads the word of the

@@ -38,7 +38,7 @@ EXPORTS = (
     "qoq_kv4_cache_bytes", "qoq_kv4_quantize", "qoq_kv4_attention_workspace_bytes",
     "qoq_kv4_decode_attention",
     "qoq_kv4_paged_bytes", "qoq_kv4_paged_append", "qoq_kv4_paged_attention_workspace_bytes",
-    "qoq_kv4_paged_attention",
+    "qoq_kv4_paged_attention", "qoq_lora_workspace_bytes", "qoq_lora_add",
 )
 
 _lock = threading.Lock()
@@ -129,6 +129,10 @@ def lib() -> ctypes.CDLL:
             L.qoq_kv4_paged_attention.restype = I
             L.qoq_kv4_paged_attention.argtypes = [P, sz, I, I, I, I, P, P, P, P, P, I, P, I, I, I,
                                                   I, ctypes.c_float, P, P, sz, P]
+            L.qoq_lora_workspace_bytes.restype = sz
+            L.qoq_lora_workspace_bytes.argtypes = [I] * 5
+            L.qoq_lora_add.restype = I
+            L.qoq_lora_add.argtypes = [P, P, I, I, I, P, P, I, I, P, P, P, P, sz, P]
             L.qoq_device_error.restype = I
             L.qoq_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint), I]
             _lib = L
@@ -871,17 +875,60 @@ def w4a8_linear_fused(X, packed, s1, N: int, group: int = 128, out=None, scratch
     return Y
 
 
+def lora_workspace_bytes(T: int, K: int, N: int, R: int, n: int) -> int:
+    return int(lib().qoq_lora_workspace_bytes(T, K, N, R, n))
+
+
+def lora_add(Y, X, A, B, ids, scaling, out=None, ws=None, stream=None):
+    """Y[t] + scaling[a] * B[a] @ (A[a] @ X[t]) with a = ids[t] (Y[t] where
+    ids[t] is outside [0, n)): the adapters of every row's request beside a
+    shared projection.
+
+    Y (T, N), X (T, K), A (n, R, K), B (n, N, R) float16, ids (T,) int32,
+    scaling (n,) float32.  out: a (T, N) float16 tensor, which may be Y
+    (default: a new one)."""
+    import torch
+    _need_cuda(X, "X", torch.float16, 2)
+    T, K = X.shape
+    dev = X.device
+    _need_cuda(A, "A", torch.float16, 3, device=dev)
+    n, R = A.shape[:2]
+    _need_cuda(Y, "Y", torch.float16, 2, device=dev)
+    N = Y.shape[1]
+    _need_cuda(Y, "Y", shape=(T, N))
+    _need_cuda(A, "A", shape=(n, R, K))
+    _need_cuda(B, "B", torch.float16, shape=(n, N, R), device=dev)
+    _need_cuda(ids, "ids", torch.int32, shape=(T,), device=dev)
+    _need_cuda(scaling, "scaling", torch.float32, shape=(n,), device=dev)
+    _need_ws(ws, dev)
+    with _on(X, stream) as s:
+        out = _out(out, (T, N), torch.float16, dev)
+        if ws is None:
+            ws = torch.empty(lora_workspace_bytes(T, K, N, R, n), dtype=torch.uint8, device=dev)
+        w, wb = _ws_args(ws)
+        _check(lib().qoq_lora_add(_ptr(Y), _ptr(X), T, K, N, _ptr(A), _ptr(B), R, n, _ptr(ids),
+                                  _ptr(scaling), _ptr(out), w, wb, s), "qoq_lora_add")
+    return out
+
+
 class QoQLinear:
     """A linear layer y = x W^T with W stored in the packed W4 format.
 
     Calling it quantizes the activations per token and runs the W4A8 GEMM;
-    both steps are CUDA kernels of ``libqoq.so``."""
+    both steps are CUDA kernels of ``libqoq.so``.  With ``adapters`` = (A, B,
+    scaling) and ``ids``, every row's low-rank adapter is added (lora_add)."""
 
     def __init__(self, W, group: int = 128):
         self.N, self.K = W.shape
         self.group = group
         self.packed, self.s1 = quantize_weights(W, group)
 
-    def __call__(self, X, out=None, scratch=None, stream=None):
-        return w4a8_linear(X, self.packed, self.s1, self.N, self.group, out=out,
-                           scratch=scratch, stream=stream)
+    def __call__(self, X, out=None, scratch=None, stream=None, adapters=None, ids=None):
+        if (adapters is None) != (ids is None):
+            raise ValueError("adapters and ids go together")
+        Y = w4a8_linear(X, self.packed, self.s1, self.N, self.group, out=out,
+                        scratch=scratch, stream=stream)
+        if adapters is not None:
+            A, B, scaling = adapters
+            lora_add(Y, X, A, B, ids, scaling, out=Y, stream=stream)
+        return Y
