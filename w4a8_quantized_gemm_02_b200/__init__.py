@@ -12,6 +12,8 @@ raised.
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 import threading
 
@@ -54,6 +56,8 @@ class QoQError(RuntimeError):
 def lib() -> ctypes.CDLL:
     """Load ``libqoq.so`` (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -467,26 +471,45 @@ def kv4_decode_attention(Q, cache, seqlen, out=None, ws=None, stream=None):
 # paged 4-bit KV cache
 # ---------------------------------------------------------------------------
 
-class _on:
-    """The device of `t` as the current one, and the stream of a call on it:
-    the caller's, or the device's current stream.  Outputs and workspaces are
-    allocated inside, so they belong to that stream."""
+def _on(t, stream):
+    """A context with the device of `t` as the current one and `stream` (if one
+    is given) as its current stream."""
+    import contextlib
 
-    def __init__(self, t, stream):
-        import torch
-        if stream is not None and stream.device != t.device:
-            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
-        self._device = torch.cuda.device(t.device)
-        self._stream = torch.cuda.stream(stream)
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError("the inputs must be CUDA tensors")
+    if stream is not None and stream.device != t.device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+    stack = contextlib.ExitStack()
+    stack.enter_context(torch.cuda.device(t.device))
+    stack.enter_context(torch.cuda.stream(stream))
+    return stack
 
-    def __enter__(self):
-        self._device.__enter__()
-        self._stream.__enter__()
-        return _stream()
 
-    def __exit__(self, *exc):
-        self._stream.__exit__(*exc)
-        self._device.__exit__(*exc)
+def _elsewhere(t, stream):
+    """Whether a call on `t` is not simply one on the current device's current
+    stream.  Such a call is made again inside _on, so that its outputs and
+    workspace belong to the stream it runs on."""
+    import torch
+    return stream is not None or t.get_device() != torch.cuda.current_device()
+
+
+def _current_stream(device: int) -> int:
+    """The address of a device's current stream."""
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(device)
+    except AttributeError:   # the public way, which takes 20 times as long
+        return torch.cuda.current_stream(device).cuda_stream
+
+
+def _need(t, name, dtype, shape, dev):
+    """_need_cuda of a dtype, shape and device, quick for a tensor that has
+    them: these calls take a few microseconds on the device."""
+    if not (getattr(t, "dtype", None) is dtype and t.device == dev and t.shape == shape
+            and t.is_contiguous() and t.is_cuda):
+        _need_cuda(t, name, dtype, shape=shape, device=dev)
 
 
 def _need_rows(t, name, dtype, width, device=None):
@@ -500,6 +523,8 @@ def _need_rows(t, name, dtype, width, device=None):
     if device is not None and t.device != device:
         raise ValueError(f"{name} is on {t.device}, expected {device}")
     rows, at = t.shape[0], 1
+    if t.is_contiguous() and rows * width == t.numel() and rows:
+        return rows, width
     for size, step in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
         if size != 1 and step != at:
             raise ValueError(f"{name}: the elements of a row must be contiguous")
@@ -513,24 +538,26 @@ def _need_rows(t, name, dtype, width, device=None):
     return rows, ld
 
 
-def _need_batch(cache, q_start, seqlen, block_table, device):
+def _need_batch(cache, q_start, seqlen, block_table, dev):
     """Checks a paged cache and a ragged batch; returns (pages, Hkv, page, B, width)."""
     import torch
     kc, vc, sc = cache
-    _need_cuda(sc, "scales", torch.float16, 4, device=device)
-    pages, Hkv, page, four = sc.shape
-    if four != 4 or page % 16:
+    shape = getattr(sc, "shape", ())
+    if len(shape) != 4 or shape[3] != 4 or shape[2] % 16:
         raise ValueError("scales must have shape (pages, Hkv, page, 4), page a multiple of 16")
+    pages, Hkv, page, _ = shape
+    _need(sc, "scales", torch.float16, shape, dev)
     shape = (pages, Hkv, page // 16, 1024)
-    _need_cuda(kc, "k_codes", torch.uint8, shape=shape, device=device)
-    _need_cuda(vc, "v_codes", torch.uint8, shape=shape, device=device)
-    _need_cuda(seqlen, "seqlen", torch.int32, 1, device=device)
-    B = seqlen.shape[0]
-    _need_cuda(q_start, "q_start", torch.int32, shape=(B + 1,), device=device)
-    _need_cuda(block_table, "block_table", torch.int32, 2, device=device)
-    if block_table.shape[0] != B:
-        raise ValueError(f"block_table must have {B} rows, got {block_table.shape[0]}")
-    return pages, Hkv, page, B, block_table.shape[1]
+    _need(kc, "k_codes", torch.uint8, shape, dev)
+    _need(vc, "v_codes", torch.uint8, shape, dev)
+    shape = getattr(block_table, "shape", ())
+    if len(shape) != 2:
+        raise ValueError("block_table must have 2 dims")
+    B, width = shape
+    _need(block_table, "block_table", torch.int32, shape, dev)
+    _need(seqlen, "seqlen", torch.int32, (B,), dev)
+    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
+    return pages, Hkv, page, B, width
 
 
 def kv4_paged_bytes(pages: int, Hkv: int, page: int, d: int = 128):
@@ -570,8 +597,6 @@ def rope_frequencies(rot: int = 128, base: float = 10000.0, scaling=None, device
                 attention_factor (0.1 ln factor + 1): pairs that turn less than
                 beta_slow times over the trained length divided, more than
                 beta_fast times kept, a ramp between."""
-    import math
-
     import torch
     if rot <= 0 or rot > 128 or rot % 16:
         raise ValueError("rot must be a multiple of 16 in 16 .. 128")
@@ -621,6 +646,7 @@ def rope_frequencies(rot: int = 128, base: float = 10000.0, scaling=None, device
     return torch.tensor(freq, dtype=torch.float64, device=device), attention
 
 
+_DEFAULT_SCALE = 1.0 / math.sqrt(128.0)
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 
 
@@ -641,24 +667,33 @@ def kv4_paged_append(qkv, cache, q_start, seqlen, block_table, Hq: int, inv_freq
         raise ValueError(f"rope_layout must be one of {sorted(_ROPE_LAYOUTS)}")
     if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda:
         raise ValueError("qkv must be a CUDA tensor")
+    if _elsewhere(qkv, stream):
+        with _on(qkv, stream):
+            return kv4_paged_append(qkv, cache, q_start, seqlen, block_table, Hq, inv_freq,
+                                    rope_layout, rope_factor, q_out, values)
     dev = qkv.device
     pages, Hkv, page, B, width = _need_batch(cache, q_start, seqlen, block_table, dev)
     T, ld = _need_rows(qkv, "qkv", torch.float16, (Hq + 2 * Hkv) * 128)
-    rot = 0
+    rot = freq = k_at = v_at = 0
     if inv_freq is not None:
         _need_cuda(inv_freq, "inv_freq", torch.float64, 1, device=dev)
-        rot = 2 * inv_freq.shape[0]
-    kh, vh = values if values is not None else (None, None)
-    for t, name in ((kh, "values[0]"), (vh, "values[1]")):
-        if values is not None:
-            _need_cuda(t, name, torch.float16, shape=(T, Hkv, 128), device=dev)
-    with _on(qkv, stream) as s:
-        q_out = _out(q_out, (T, Hq, 128), torch.float16, dev)
-        _check(lib().qoq_kv4_paged_append(
-            _ptr(qkv), ld, T, Hq, Hkv, 128, _ptr(q_start), _ptr(seqlen), B, _ptr(block_table),
-            width, pages, page, _ptr(inv_freq), rot, _ROPE_LAYOUTS[rope_layout],
-            float(rope_factor), _ptr(q_out), _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]),
-            _ptr(kh), _ptr(vh), s), "qoq_kv4_paged_append")
+        rot, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
+    if values is not None:
+        kh, vh = values
+        _need(kh, "values[0]", torch.float16, (T, Hkv, 128), dev)
+        _need(vh, "values[1]", torch.float16, (T, Hkv, 128), dev)
+        k_at, v_at = kh.data_ptr(), vh.data_ptr()
+    if q_out is None:
+        q_out = torch.empty((T, Hq, 128), dtype=torch.float16, device=dev)
+    else:
+        _need(q_out, "q_out", torch.float16, (T, Hq, 128), dev)
+    st = lib().qoq_kv4_paged_append(
+        qkv.data_ptr(), ld, T, Hq, Hkv, 128, q_start.data_ptr(), seqlen.data_ptr(), B,
+        block_table.data_ptr(), width, pages, page, freq, rot, _ROPE_LAYOUTS[rope_layout],
+        rope_factor, q_out.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(),
+        cache[2].data_ptr(), k_at, v_at, _current_stream(dev.index))
+    if st:
+        _check(st, "qoq_kv4_paged_append")
     return q_out
 
 
@@ -671,28 +706,49 @@ def kv4_paged_attention(Q, cache, q_start, seqlen, block_table, max_q=None, scal
     number of rows of a sequence (1 for a decode step; default: T).  scale:
     default 1 / sqrt(128).  ws: a uint8 workspace of
     kv4_paged_attention_workspace_bytes (default: allocated for the call)."""
-    import math
-
     import torch
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.shape[2] != 128:
         raise ValueError("Q must have shape (T, Hq, 128)")
+    if not Q.is_cuda:
+        raise ValueError("Q must be a CUDA tensor")
+    if _elsewhere(Q, stream):
+        with _on(Q, stream):
+            return kv4_paged_attention(Q, cache, q_start, seqlen, block_table, max_q, scale, out,
+                                       ws)
     Hq, dev = Q.shape[1], Q.device
     T, ldq = _need_rows(Q, "Q", torch.float16, Hq * 128)
     pages, Hkv, page, B, width = _need_batch(cache, q_start, seqlen, block_table, dev)
-    max_q = max(T, 1) if max_q is None else int(max_q)
-    scale = 1.0 / math.sqrt(128.0) if scale is None else float(scale)
-    _need_ws(ws, dev)
-    with _on(Q, stream) as s:
-        out = _out(out, (T, Hq, 128), torch.float16, dev)
-        if ws is None:
-            need = kv4_paged_attention_workspace_bytes(T, Hq, Hkv, B, width, page, max_q)
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-        w, wb = _ws_args(ws)
-        _check(lib().qoq_kv4_paged_attention(
-            _ptr(Q), ldq, T, Hq, Hkv, 128, _ptr(cache[0]), _ptr(cache[1]), _ptr(cache[2]),
-            _ptr(q_start), _ptr(seqlen), B, _ptr(block_table), width, pages, page, max_q, scale,
-            _ptr(out), w, wb, s), "qoq_kv4_paged_attention")
+    max_q = max(T, 1) if max_q is None else max_q
+    scale = _DEFAULT_SCALE if scale is None else scale
+    if out is None:
+        out = torch.empty((T, Hq, 128), dtype=torch.float16, device=dev)
+    else:
+        _need(out, "out", torch.float16, (T, Hq, 128), dev)
+    if ws is None:
+        ws = torch.empty(_attention_ws(dev.index, T, Hq, Hkv, B, width, page, max_q),
+                         dtype=torch.uint8, device=dev)
+    else:
+        _need_ws(ws, dev)
+    st = lib().qoq_kv4_paged_attention(
+        Q.data_ptr(), ldq, T, Hq, Hkv, 128, cache[0].data_ptr(), cache[1].data_ptr(),
+        cache[2].data_ptr(), q_start.data_ptr(), seqlen.data_ptr(), B, block_table.data_ptr(),
+        width, pages, page, max_q, scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
+        _current_stream(dev.index))
+    if st:
+        _check(st, "qoq_kv4_paged_attention")
     return out
+
+
+@functools.lru_cache(maxsize=256)
+def _attention_ws(device, T, Hq, Hkv, B, width, page, max_q):
+    """kv4_paged_attention_workspace_bytes on the current device (its number is
+    only a key: the size depends on the SM count)."""
+    return kv4_paged_attention_workspace_bytes(T, Hq, Hkv, B, width, page, max_q)
+
+
+@functools.lru_cache(maxsize=256)
+def _lora_ws(device, T, K, N, R, n):
+    return lora_workspace_bytes(T, K, N, R, n)
 
 
 def kv4_paged_attention_workspace_bytes(T: int, Hq: int, Hkv: int, B: int, width: int, page: int,
@@ -888,26 +944,35 @@ def lora_add(Y, X, A, B, ids, scaling, out=None, ws=None, stream=None):
     scaling (n,) float32.  out: a (T, N) float16 tensor, which may be Y
     (default: a new one)."""
     import torch
-    _need_cuda(X, "X", torch.float16, 2)
-    T, K = X.shape
-    dev = X.device
-    _need_cuda(A, "A", torch.float16, 3, device=dev)
-    n, R = A.shape[:2]
-    _need_cuda(Y, "Y", torch.float16, 2, device=dev)
-    N = Y.shape[1]
-    _need_cuda(Y, "Y", shape=(T, N))
-    _need_cuda(A, "A", shape=(n, R, K))
-    _need_cuda(B, "B", torch.float16, shape=(n, N, R), device=dev)
-    _need_cuda(ids, "ids", torch.int32, shape=(T,), device=dev)
-    _need_cuda(scaling, "scaling", torch.float32, shape=(n,), device=dev)
-    _need_ws(ws, dev)
-    with _on(X, stream) as s:
-        out = _out(out, (T, N), torch.float16, dev)
-        if ws is None:
-            ws = torch.empty(lora_workspace_bytes(T, K, N, R, n), dtype=torch.uint8, device=dev)
-        w, wb = _ws_args(ws)
-        _check(lib().qoq_lora_add(_ptr(Y), _ptr(X), T, K, N, _ptr(A), _ptr(B), R, n, _ptr(ids),
-                                  _ptr(scaling), _ptr(out), w, wb, s), "qoq_lora_add")
+    if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2:
+        raise ValueError("X must be a CUDA tensor with 2 dims")
+    if _elsewhere(X, stream):
+        with _on(X, stream):
+            return lora_add(Y, X, A, B, ids, scaling, out, ws)
+    (T, K), dev = X.shape, X.device
+    shape = getattr(B, "shape", ())
+    if len(shape) != 3:
+        raise ValueError("B must have 3 dims")
+    n, N, R = shape
+    _need(X, "X", torch.float16, (T, K), dev)
+    _need(Y, "Y", torch.float16, (T, N), dev)
+    _need(A, "A", torch.float16, (n, R, K), dev)
+    _need(B, "B", torch.float16, shape, dev)
+    _need(ids, "ids", torch.int32, (T,), dev)
+    _need(scaling, "scaling", torch.float32, (n,), dev)
+    if out is None:
+        out = torch.empty((T, N), dtype=torch.float16, device=dev)
+    elif out is not Y:
+        _need(out, "out", torch.float16, (T, N), dev)
+    if ws is None:
+        ws = torch.empty(_lora_ws(dev.index, T, K, N, R, n), dtype=torch.uint8, device=dev)
+    else:
+        _need_ws(ws, dev)
+    st = lib().qoq_lora_add(Y.data_ptr(), X.data_ptr(), T, K, N, A.data_ptr(), B.data_ptr(), R, n,
+                            ids.data_ptr(), scaling.data_ptr(), out.data_ptr(), ws.data_ptr(),
+                            ws.numel(), _current_stream(dev.index))
+    if st:
+        _check(st, "qoq_lora_add")
     return out
 
 
