@@ -316,6 +316,9 @@ PROMPT = [
     ([300], [45], 64, 8, 1),
     ([40, 2], [3, 900], 32, 20, 1),
     ([128, 256], [0, 0], 64, 1, 1),
+    ([40, 5], [3500, 2100], 64, 4, 1),       # split over the tokens
+    ([9], [1500], 16, 17, 1),
+    ([70, 3, 20], [1100, 0, 5000], 32, 4, 1),
 ]
 
 
@@ -323,9 +326,10 @@ PROMPT = [
 def test_prompt_matches_reference(q, past, page, Hq, Hkv):
     rng = np.random.default_rng(sum(q) + sum(past))
     _check(*_run_attention(rng, q, past, page, Hq, Hkv))
+    assert qoq.device_error() == 0
 
 
-@pytest.mark.parametrize("q,past", [([1, 1], [800, 33]), ([90], [200])])
+@pytest.mark.parametrize("q,past", [([1, 1], [800, 33]), ([90], [200]), ([50], [2500])])
 def test_attention_saturated_scores(q, past):
     """Scores of hundreds: the softmax picks few tokens and its maximum keeps
     rising."""

@@ -100,6 +100,28 @@ def test_tile_slots_hold_every_sequence(idx):
         assert base[-1] <= int(start[-1]) * g // tile + len(q)
 
 
+def test_splits_fit_the_grid_and_the_workspace():
+    """The rule by which the kernels split sequences, over random batches: units
+    of equal length `chunk`, at least the batch's work over `target`.  No batch has
+    more units than target + pairs, nor more units of split sequences (the ones
+    that leave partial results) than 2 target; every unit has work."""
+    rng = np.random.default_rng(2)
+    for target, least in ((8 * 148, 32), (148, 8)):
+        for _ in range(400):
+            B, Hkv = int(rng.integers(1, 200)), int(rng.integers(1, 65))
+            top = int(10 ** rng.uniform(0, 4.2))
+            n = rng.integers(0, top + 1, B)
+            if rng.random() < 0.3:
+                n[rng.integers(0, B)] = 100000
+            chunk = max(least, -(-int(n.sum()) * Hkv // target))
+            splits = np.where(n <= chunk, 1, -(-n // chunk))
+            assert splits.sum() * Hkv <= target + B * Hkv
+            assert (splits[splits > 1].sum() * Hkv) <= 2 * target
+            for m, k in zip(n[splits > 1], splits[splits > 1]):
+                per = -(-int(m) // int(k))
+                assert per <= chunk and (k - 1) * per < m and (k - 1) * chunk < m
+
+
 def test_nibble_tables_are_permutations():
     for at in (ref.K_AT, ref.V_AT):
         assert sorted(at.tolist()) == list(range(2048))

@@ -27,20 +27,26 @@ struct PagedArgs {
   float* parts;             // per unit and row: a partial result (kPartFloats)
 };
 
-// A sequence with at most kDecodeRows<nt> rows (query tokens x g) runs in the
-// decode kernel with 8 nt columns, a longer one in the prompt kernel.
+// A sequence with at most 8 nt rows (query tokens x g) runs in the decode
+// kernel, a longer one in the prompt kernel.
 struct PagedPlan {
   int nt;                   // 8-column tiles of the decode kernel: 1, 2, or 0 (not launched)
   int target;               // splits it aims at for the whole batch
   int grid;
   bool combine;             // a sequence may be split
   bool prompt;              // sequences with more rows may be there
-  int tiles;                // prompt: row-tile slots of the batch
-  int prompt_target;        // prompt: splits aimed at (0: never split)
-  int prompt_grid;
+  int tiles;                // prompt: row slots of the batch
+  int prompt_target, prompt_grid;
+  bool prompt_combine;
   size_t meta_off, parts_off, prompt_meta_off, prompt_parts_off, bytes;
+  size_t take(size_t n) {   // the workspace's next n bytes
+    const size_t off = bytes;
+    bytes += (n + 255) / 256 * 256;
+    return off;
+  }
 };
 PagedPlan paged_plan(int T, int B, int Hq, int Hkv, int width, int page, int max_q);
+void plan_prompt(PagedPlan& p, int T, int B, int Hq, int Hkv, int width, int page);
 
 int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, cudaStream_t s);
 

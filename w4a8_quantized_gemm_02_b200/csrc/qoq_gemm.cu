@@ -1717,5 +1717,5 @@ extern "C" int qoq_device_error(unsigned int* value, int clear) {
     if (cudaMemcpyToSymbol(g_error_word, &zero, sizeof(unsigned int)) != cudaSuccess)
       return QOQ_ERR_CUDA;
   }
-  return QOQ_OK;
+  return prompt_device_error(value, clear);
 }

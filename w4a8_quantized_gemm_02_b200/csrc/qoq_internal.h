@@ -69,6 +69,10 @@ int launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_
   return QOQ_OK;
 }
 
+// The prompt attention's part of the device error word: ORed into *value and,
+// with `clear`, set to zero.
+int prompt_device_error(unsigned int* value, int clear);
+
 // Checks shared by the entry points over a paged cache (qoq_append.cu).
 int check_paged_shape(int pages, int Hkv, int page, int d);
 int check_batch(int T, int B, int width, int page);

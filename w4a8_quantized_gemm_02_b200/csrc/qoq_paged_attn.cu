@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(kThreads)
 paged_decode_kernel(const PagedArgs a, int target) {
   __shared__ __align__(16) uint8_t smem[kWarps * kStages * kStageBytes];
   __shared__ long long s_sum[kWarps];
-  __shared__ int s_scan[kWarps];
-  __shared__ int s_unit[3];
+  __shared__ int2 s_scan[kWarps];
+  __shared__ int s_unit[4];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   grid_dependency_wait();
@@ -101,30 +101,40 @@ paged_decode_kernel(const PagedArgs a, int target) {
   long long want = (sum * a.Hkv + target - 1) / target;
   want = (want + kWarps - 1) / kWarps * kWarps;
   const int chunk = static_cast<int>(want < kMinBlocks ? kMinBlocks : want);
-  int base = 0;
+  int base = 0, pbase = 0;
   for (int b0 = 0; b0 < a.B && base <= u; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
     const int n = b0 == 0 ? n0 : (b < a.B ? blocks_of(a, b, 8 * NT) : -1);
     const int nsplit = n < 0 ? 0 : (n <= chunk ? 1 : (n + chunk - 1) / chunk);
-    int incl = nsplit * a.Hkv;
+    const int mine = nsplit * a.Hkv, parts = nsplit > 1 ? mine : 0;
+    int incl = mine, pincl = parts;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += up;
+      const int pup = __shfl_up_sync(0xffffffffu, pincl, o);
+      if (lane >= o) {
+        incl += up;
+        pincl += pup;
+      }
     }
-    if (lane == 31) s_scan[warp] = incl;
+    if (lane == 31) s_scan[warp] = make_int2(incl, pincl);
     __syncthreads();
-    int before = base;
+    int before = base, pbefore = pbase;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s_scan[w];
-      base += s_scan[w];
+      if (w < warp) {
+        before += s_scan[w].x;
+        pbefore += s_scan[w].y;
+      }
+      base += s_scan[w].x;
+      pbase += s_scan[w].y;
     }
-    const int first = before + incl - nsplit * a.Hkv;
-    if (u >= first && u < before + incl) {
+    const int off = u - (before + incl - mine);
+    if (off >= 0 && off < mine) {
       s_unit[0] = b;
-      s_unit[1] = u - first;
+      s_unit[1] = off;
       s_unit[2] = nsplit;
+      s_unit[3] = pbefore + pincl - parts + off;    // its number among the split ones
     }
     __syncthreads();
   }
@@ -207,7 +217,6 @@ paged_decode_kernel(const PagedArgs a, int target) {
     }
   }
   const int all_see = visible(position_of(a.seqlen[b], rr.n, 0), Lb);
-  const bool more_rows = R < 8 * NT;   // rows past R never raise the maximum
 
   float acc[NT][8][4];
   float mrun[NT][2], lsum[NT][2], osum[NT][2];
@@ -223,7 +232,6 @@ paged_decode_kernel(const PagedArgs a, int target) {
       lsum[nt][c] = osum[nt][c] = 0.0f;
     }
   }
-  (void)more_rows;
 
   uint32_t absent = 0;    // of 32 iterations: the blocks whose page is not in the pool
   for (int it = 0; it < niter; ++it) {
@@ -382,7 +390,7 @@ paged_decode_kernel(const PagedArgs a, int target) {
   __syncthreads();
   const int pair = b * a.Hkv + hk;
   if (threadIdx.x == 0 && split == 0 && a.meta != nullptr)
-    a.meta[pair] = make_int2(static_cast<int>(u), nsplit);
+    a.meta[pair] = make_int2(s_unit[3], nsplit);
   // 16 threads a row, 8 dimensions each
   const int d0 = 8 * (threadIdx.x & 15);
 #pragma unroll
@@ -413,7 +421,7 @@ paged_decode_kernel(const PagedArgs a, int target) {
       store_row8(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * g + (r - qi * g)) *
                              kHeadDim + d0, v, den == den ? inv : den);
     } else {
-      float* part = a.parts + (static_cast<size_t>(u) * (8 * NT) + r) * kPartFloats;
+      float* part = a.parts + (static_cast<size_t>(s_unit[3]) * (8 * NT) + r) * kPartFloats;
       if ((threadIdx.x & 15) == 0) {
         part[0] = M;
         part[1] = den;
@@ -522,12 +530,6 @@ PagedPlan paged_plan(int T, int B, int Hq, int Hkv, int width, int page, int max
   if (most > 8 && most <= 16) p.nt = 2;
   p.prompt = most > 8 * p.nt;
   const long long blocks = (static_cast<long long>(width) * page + 15) / 16;
-  size_t at = 0;
-  auto take = [&](size_t bytes) {
-    const size_t off = at;
-    at += (bytes + 255) / 256 * 256;
-    return off;
-  };
   if (p.nt) {
     const long long most_splits = (blocks + kMinBlocks - 1) / kMinBlocks;
     p.target = 8 * sm_count();
@@ -535,11 +537,16 @@ PagedPlan paged_plan(int T, int B, int Hq, int Hkv, int width, int page, int max
     p.grid = static_cast<int>(a < b ? a : b);
     p.combine = most_splits > 1;
     if (p.combine) {
-      p.meta_off = take(static_cast<size_t>(pairs) * sizeof(int2));
-      p.parts_off = take(static_cast<size_t>(p.grid) * 8 * p.nt * kPartFloats * sizeof(float));
+      // A sequence is split where its length n is over chunk >= blocks * Hkv / target
+      // (all in blocks), into fewer than n / chunk + 1 < 2 n / chunk: at most 2 target
+      // units of the batch leave partial results.
+      const long long split = 2LL * p.target;
+      const long long parts = split < p.grid ? split : p.grid;
+      p.meta_off = p.take(static_cast<size_t>(pairs) * sizeof(int2));
+      p.parts_off = p.take(static_cast<size_t>(parts) * 8 * p.nt * kPartFloats * sizeof(float));
     }
   }
-  p.bytes = at;
+  if (p.prompt) plan_prompt(p, T, B, Hq, Hkv, width, page);
   return p;
 }
 
@@ -612,8 +619,8 @@ extern "C" int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq,
     if (st) return st;
   }
   if (p.prompt) {
-    a.meta = reinterpret_cast<int2*>(w + p.prompt_meta_off);
-    a.parts = reinterpret_cast<float*>(w + p.prompt_parts_off);
+    a.meta = p.prompt_combine ? reinterpret_cast<int2*>(w + p.prompt_meta_off) : nullptr;
+    a.parts = p.prompt_combine ? reinterpret_cast<float*>(w + p.prompt_parts_off) : nullptr;
     return launch_paged_prompt(a, p, 8 * p.nt + 1, s);
   }
   return QOQ_OK;
