@@ -100,26 +100,65 @@ def test_tile_slots_hold_every_sequence(idx):
         assert base[-1] <= int(start[-1]) * g // tile + len(q)
 
 
-def test_splits_fit_the_grid_and_the_workspace():
-    """The rule by which the kernels split sequences, over random batches: units
+def test_prompt_splits_fit_the_grid_and_the_workspace():
+    """The rule by which the prompt kernel splits slots, over random batches: units
     of equal length `chunk`, at least the batch's work over `target`.  No batch has
-    more units than target + pairs, nor more units of split sequences (the ones
-    that leave partial results) than 2 target; every unit has work."""
+    more units than target + pairs, nor more units of split slots (the ones that
+    leave partial results) than 2 target; every unit has work."""
     rng = np.random.default_rng(2)
-    for target, least in ((8 * 148, 32), (148, 8)):
-        for _ in range(400):
-            B, Hkv = int(rng.integers(1, 200)), int(rng.integers(1, 65))
-            top = int(10 ** rng.uniform(0, 4.2))
-            n = rng.integers(0, top + 1, B)
-            if rng.random() < 0.3:
-                n[rng.integers(0, B)] = 100000
-            chunk = max(least, -(-int(n.sum()) * Hkv // target))
-            splits = np.where(n <= chunk, 1, -(-n // chunk))
-            assert splits.sum() * Hkv <= target + B * Hkv
-            assert (splits[splits > 1].sum() * Hkv) <= 2 * target
-            for m, k in zip(n[splits > 1], splits[splits > 1]):
-                per = -(-int(m) // int(k))
-                assert per <= chunk and (k - 1) * per < m and (k - 1) * chunk < m
+    target, least = 148, 8
+    for _ in range(400):
+        B, Hkv = int(rng.integers(1, 200)), int(rng.integers(1, 65))
+        n = rng.integers(0, int(10 ** rng.uniform(0, 4.2)) + 1, B)
+        if rng.random() < 0.3:
+            n[rng.integers(0, B)] = 100000
+        chunk = max(least, -(-int(n.sum()) * Hkv // target))
+        splits = np.where(n <= chunk, 1, -(-n // chunk))
+        assert splits.sum() * Hkv <= target + B * Hkv
+        assert (splits[splits > 1].sum() * Hkv) <= 2 * target
+        for m, k in zip(n[splits > 1], splits[splits > 1]):
+            per = -(-int(m) // int(k))
+            assert per <= chunk and (k - 1) * per < m and (k - 1) * chunk < m
+
+
+def test_decode_runs_cover_every_pair_once():
+    """The decode kernel's runs, over random batches: with every pair's length in
+    blocks and a constant in front of it, a CTA's run is cut at the pairs' ends;
+    every block is in one piece, and a pair's unfinished pieces are the last of its
+    first CTA and the first of the next ones, where the merge looks for them."""
+    rng = np.random.default_rng(3)
+    cost = 12
+    for grid in (1, 7, 592):
+        for _ in range(60):
+            B, Hkv = int(rng.integers(1, 40)), int(rng.integers(1, 9))
+            n = rng.integers(0, int(10 ** rng.uniform(0, 3)) + 1, B)
+            w = np.maximum(n, 1) + cost
+            total, mean = int(w.sum()) * Hkv, -(-int(w.sum()) // len(w))
+            run = max(-(-total // grid), min(cost + 16, mean))
+            assert run * grid >= total
+            places, at = set(), 0
+            for b, m in enumerate(w):
+                for h in range(Hkv):
+                    lo, hi = at, at + int(m)
+                    at = hi
+                    pieces = []
+                    for k in range(lo // run, (hi - 1) // run + 1):
+                        assert k < grid
+                        f, t = max(lo, k * run) - lo, min(hi, (k + 1) * run) - lo
+                        c0, c1 = max(0, f - cost), t - cost
+                        if c1 > 0:
+                            pieces.append((k, c0, c1, c0 == 0 and t == hi - lo))
+                    first, last = pieces[0][0], (hi - 1) // run
+                    assert [p[0] for p in pieces] == list(range(first, last + 1))
+                    assert pieces[0][1] == 0 and pieces[-1][2] == m - cost
+                    assert all(p[2] == q[1] for p, q in zip(pieces, pieces[1:]))
+                    assert pieces[0][3] == (first == last)
+                    for k, c0, _, whole in pieces:
+                        if not whole:
+                            place = 2 * k + (c0 == 0)
+                            assert place not in places and place < 2 * grid
+                            assert place == (2 * first + 1 if k == first else 2 * k)
+                            places.add(place)
 
 
 def test_nibble_tables_are_permutations():
@@ -196,7 +235,6 @@ def test_workspace_is_bounded_and_zero_for_nothing(L):
     assert f(0, 4, 1, 128, 2, 64, 16, 1) == 0
     assert f(4, 4, 1, 128, 0, 64, 16, 1) == 0
     assert f(4, 4, 3, 128, 2, 64, 16, 1) == 0       # an invalid shape
-    assert f(4, 4, 1, 128, 2, 2, 16, 1) == 0        # sequences too short to be split
     for B in (1, 64, 4096):
         # partial results of the splits: some thousand units of at most 16 rows
         assert f(B, 32, 8, 128, B, 8192, 16, 1) <= (16 * 148 + 8 * B) * 8 * 528 + (8 * B + 64) * 8

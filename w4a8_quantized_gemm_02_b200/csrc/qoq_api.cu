@@ -58,6 +58,27 @@ int sm_count() {
   return sms;
 }
 
+int opt_in_smem(const void* kernel, size_t smem, std::atomic<unsigned long long>& ready,
+                int min_regs) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return QOQ_ERR_CUDA;
+  }
+  const unsigned long long bit = dev >= 0 && dev < kMaxDevices ? 1ull << dev : 0;
+  if (ready.load(std::memory_order_relaxed) & bit) return QOQ_OK;
+  cudaFuncAttributes attr;
+  if (cudaFuncGetAttributes(&attr, kernel) != cudaSuccess ||
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(smem)) != cudaSuccess) {
+    cudaGetLastError();
+    return QOQ_ERR_CUDA;
+  }
+  if (attr.numRegs < min_regs) return QOQ_ERR_UNSUPPORTED;
+  ready.fetch_or(bit, std::memory_order_relaxed);
+  return QOQ_OK;
+}
+
 int launch_status() {
   return cudaGetLastError() == cudaSuccess ? QOQ_OK : QOQ_ERR_CUDA;
 }

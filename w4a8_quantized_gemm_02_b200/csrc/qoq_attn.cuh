@@ -23,17 +23,17 @@ struct PagedArgs {
   int T, B, Hq, Hkv, g, width, pages, page, max_q;
   float scale;
   __half* out;              // T x Hq x 128
-  int2* meta;               // per (sequence, KV head): first unit and splits
-  float* parts;             // per unit and row: a partial result (kPartFloats)
+  int2* meta;               // decode: per (sequence, KV head), its first and last CTA;
+                            // prompt: per (slot, KV head), its first part and their number
+  float* parts;             // partial results, kPartFloats a row
 };
 
-// A sequence with at most 8 nt rows (query tokens x g) runs in the decode
+// A sequence with at most 4 nt rows (query tokens x g) runs in the decode
 // kernel, a longer one in the prompt kernel.
 struct PagedPlan {
-  int nt;                   // 8-column tiles of the decode kernel: 1, 2, or 0 (not launched)
-  int target;               // splits it aims at for the whole batch
-  int grid;
-  bool combine;             // a sequence may be split
+  int nt;                   // four-row tiles of the decode kernel: 1, 2, 4, or 0 (not launched)
+  int grid;                 // its CTAs
+  bool combine;             // a (sequence, KV head) pair may lie in several of them
   bool prompt;              // sequences with more rows may be there
   int tiles;                // prompt: row slots of the batch
   int prompt_target, prompt_grid;
@@ -50,7 +50,11 @@ void plan_prompt(PagedPlan& p, int T, int B, int Hq, int Hkv, int width, int pag
 
 int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, cudaStream_t s);
 
-// 8 outputs times `f`, rounded to FP16.
+// 4 or 8 outputs times `f`, rounded to FP16.
+__device__ __forceinline__ void store_row4(__half* dst, float4 v, float f) {
+  const __half2 o[2] = {__floats2half2_rn(v.x * f, v.y * f), __floats2half2_rn(v.z * f, v.w * f)};
+  *reinterpret_cast<uint2*>(dst) = *reinterpret_cast<const uint2*>(o);
+}
 __device__ __forceinline__ void store_row8(__half* dst, const float (&v)[8], float f) {
   __half2 o[4];
 #pragma unroll

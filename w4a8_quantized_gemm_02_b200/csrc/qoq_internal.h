@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "qoq.h"
 
 namespace qoq {
@@ -68,6 +70,12 @@ int launch_dependent(void (*kernel)(Params...), dim3 grid, unsigned block, size_
   }
   return QOQ_OK;
 }
+
+// Opt a kernel in to `smem` bytes of dynamic shared memory, once per device
+// (`ready`: a bit per device, one variable per kernel).  QOQ_ERR_UNSUPPORTED if it
+// was built with fewer than `min_regs` registers a thread.
+int opt_in_smem(const void* kernel, size_t smem, std::atomic<unsigned long long>& ready,
+                int min_regs = 0);
 
 // The prompt attention's part of the device error word: ORed into *value and,
 // with `clear`, set to zero.

@@ -63,6 +63,13 @@ __device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4],
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// (x & m) | o in one operation.
+__device__ __forceinline__ uint32_t and_or(uint32_t x, uint32_t m, uint32_t o) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(x), "r"(m), "r"(o));
+  return d;
+}
+
 // 8x8 transpose of 16-bit elements across the warp: lane 4 r + c holds row r,
 // columns 2c and 2c + 1, before and after.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {

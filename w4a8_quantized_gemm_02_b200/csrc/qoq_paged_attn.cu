@@ -1,33 +1,41 @@
 // Attention over a paged 4-bit KV cache: single tokens (decode) and the few
 // query tokens of a sequence that is verified or extended by a handful.
 //
-// Row tile.  The n query tokens of a sequence times the g = Hq / Hkv heads of a
-// KV head are the rows of one problem: row r = i g + h.  Up to 16 rows run
-// here; more go to the prompt kernel.
+// Rows.  The n query tokens of a sequence times the g = Hq / Hkv heads of a KV
+// head are the rows of one problem: row r = i g + h.  Up to 16 rows run here,
+// four to an MMA's eight columns; more go to the prompt kernel.
 //
-// Arithmetic.  With k^ = s q + m the products never leave the codes c (the
-// cache's UINT4 values, exact as FP16 subnormals c 2^-24):
+// Arithmetic.  The products run on the codes c, never on dequantized vectors.
+// With k^ = s c + m:
 //     q . k^_t = s_t (q . c_t) + m_t Q,    Q = sum_i q_i,
-//     sum_t p_t v^_t = sum_t w_t c_t + sum_t p_t m_t,    w_t = p_t s_t.
-// The weights enter the tensor cores as w~ = fp16(w), half an FP16 step (2^-12)
-// off.  Codes lie around 8, so that error times 8 would dominate where values
-// cancel; with
-//     sum w c = sum w~ (c - 8) + 8 sum w + (error: sum (w - w~)(c - 8))
-// the products stay on c, and each weight adds 8 (w - w~) to its row's FP32
-// offset sum: what is left is 2^-12 of values centred on their vector's middle,
-// no more than rounding v^ itself would cost.
+//     sum_t p_t v^_t = sum_t w_t (c_t - 8) + sum_t p_t (m_t + 8 s_t),  w_t = p_t s_t.
+// Scores: 8-bit integer MMAs, exact in INT32, with the queries as 16-bit fixed
+// point of their row (a column for the high and one for the low byte): a shift
+// and two masks unpack eight codes.  That rounds a query value to 2^-16 of its
+// row's largest, less than its own FP16 rounding for values within 32 times of
+// it; a score moves by about 3e-5 of the size of k^ where |q| stays under 4.
+// Outputs: FP16 MMAs, the weights as a high and a low FP16 column (22 bits), the
+// codes centred on 8, which keeps what the tensor cores' FP32 accumulation
+// touches as small as v^ about its vector's middle: over 131000 tokens, sums of
+// uncentred codes lost half the output's digits (5.5e-4 of it against 2.6e-4).
 //
 // The running maximum is only raised when a score passes it by 2.9 (in log2
-// units): one vote a block instead of a reduction.  2^2.9 = 7.46 times the
+// units): one vote an iteration instead of a reduction.  2^2.9 = 7.46 times the
 // largest scale of a finite FP16 vector, 131008 / 15, is still an FP16 number.
 //
-// Bound.  136 bytes a token and KV head, read once; the instructions of the
-// unpacking and of the softmax come close behind (see the figures at the
-// kernel).
+// Work.  The batch's blocks of 16 tokens, in the order of sequences, KV heads and
+// tokens, are cut into equal runs, one for each resident CTA, whatever the mix of
+// lengths.  A run covers whole (sequence, KV head) pairs, whose outputs it writes,
+// and at most one unfinished pair at either end, whose partial results a second
+// kernel merges.
+//
+// Bound.  136 bytes a token and KV head, read once; the instructions that unpack
+// them come close behind (see the figures at the kernel).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "qoq.h"
@@ -42,20 +50,37 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStages = 4;                           // per warp: blocks of 16 tokens in flight
-constexpr int kStageBytes = 1024 + 1024 + 128;       // K codes, V codes, scales of a block
-constexpr int kMinBlocks = 32;                       // a split's least length: 8 blocks a warp
+constexpr int kStages = 2;                           // per warp: iterations in flight
+constexpr int kBlockBytes = 1024 + 1024 + 128;       // K codes, V codes, scales of a block
+constexpr int kStageBytes = 2 * kBlockBytes;         // an iteration is two blocks
+constexpr int kMinBlocks = 16;                       // a run's least length
+constexpr int kPairCost = 12;                        // a pair's beginning and end, in blocks
 constexpr float kRaise = 2.9f;
-// Codes are FP16 subnormals: c 2^-24 on rows 0..7 of the 16-row operand, c 2^-20
-// on rows 8..15 (masked out of bits 4..7 without a shift).
-constexpr float kRowScale0 = 16777216.0f, kRowScale1 = 1048576.0f;
+constexpr float kFixed = 32512.0f;                   // 127 * 256: a query row's largest value
 
-__device__ __forceinline__ void a_frag(uint32_t word, uint32_t (&a)[4]) {
+// CTAs of the decode kernel on an SM, by its tiles of four rows.
+constexpr int resident_ctas(int nt) { return nt == 1 ? 4 : (nt == 2 ? 3 : 2); }
+
+__device__ __forceinline__ void mma_u8s8(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.u8.s8.s32 "
+      "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Codes minus 8: 0x6400 | c is 1024 + c, 0x5400 | 16 c is 64 + c.
+__device__ __forceinline__ uint32_t minus(uint32_t n, float k) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&n), __float2half2_rn(k));
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ void v_frag(uint32_t word, uint32_t (&a)[4]) {
   const uint32_t hi = word >> 8;
-  a[0] = word & 0x000f000fu;
-  a[1] = word & 0x00f000f0u;
-  a[2] = hi & 0x000f000fu;
-  a[3] = hi & 0x00f000f0u;
+  a[0] = minus(and_or(word, 0x000f000fu, 0x64006400u), 1032.0f);
+  a[1] = minus(and_or(word, 0x00f000f0u, 0x54005400u), 72.0f);
+  a[2] = minus(and_or(hi, 0x000f000fu, 0x64006400u), 1032.0f);
+  a[3] = minus(and_or(hi, 0x00f000f0u, 0x54005400u), 72.0f);
 }
 
 // 16-token blocks of sequence b for this kernel: 0 for an empty one that still
@@ -65,370 +90,424 @@ __device__ __forceinline__ int blocks_of(const PagedArgs& a, int b, int rows_max
   if (rr.n <= 0 || rr.n > a.max_q || rr.n * a.g > rows_max_here) return -1;
   return (clamp_len(a.seqlen[b], a.width * a.page) + 15) >> 4;
 }
+// Its share of the work for one KV head: its blocks (an empty one counts as one)
+// and kPairCost in front of them.
+__device__ __forceinline__ int weight_of(int blocks) {
+  return blocks < 0 ? 0 : kPairCost + (blocks == 0 ? 1 : blocks);
+}
 
-// Grid: `target` + B * Hkv CTAs at most; every one finds its work from the
-// lengths.  All CTAs agree on the split length `chunk` = the batch's blocks over
-// `target`, so splits are equally long whatever the mix of lengths, and a
-// sequence has as many as it needs.  Unit u is split u - base of a (sequence, KV
-// head) pair; warp w takes every fourth block of it.
+// Grid: one CTA for each that is resident.
 template <int NT>
-__global__ void __launch_bounds__(kThreads)
-paged_decode_kernel(const PagedArgs a, int target) {
-  __shared__ __align__(16) uint8_t smem[kWarps * kStages * kStageBytes];
-  __shared__ long long s_sum[kWarps];
-  __shared__ int2 s_scan[kWarps];
-  __shared__ int s_unit[4];
+__global__ void __launch_bounds__(kThreads, resident_ctas(NT))
+paged_decode_kernel(const PagedArgs a) {
+  constexpr int kRows = 4 * NT;
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ long long s_sum[kWarps], s_start;
+  __shared__ int s_b;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   grid_dependency_wait();
   grid_launch_dependents();
 
-  // --- the unit of this CTA ---
-  const int u = blockIdx.x;
-  long long sum = 0;
-  const int n0 = static_cast<int>(threadIdx.x) < a.B ? blocks_of(a, threadIdx.x, 8 * NT) : -1;
-  if (n0 > 0) sum = n0;
-  for (int b = threadIdx.x + kThreads; b < a.B; b += kThreads) {
-    const int n = blocks_of(a, b, 8 * NT);
-    if (n > 0) sum += n;
-  }
+  // --- this CTA's run: [start, end) of the batch's `total` blocks ---
+  // (counted with it: the sequences that have work, in the upper bits)
+  auto share = [&](int b) {
+    const int w = b < a.B ? weight_of(blocks_of(a, b, kRows)) : 0;
+    return w ? (1LL << 40) + w : 0LL;
+  };
+  const long long mine = share(threadIdx.x);
+  const int w0 = static_cast<int>(mine);
+  long long sum = mine;
+  for (int b = threadIdx.x + kThreads; b < a.B; b += kThreads) sum += share(b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) s_sum[warp] = sum;
-  if (threadIdx.x == 0) s_unit[0] = -1;
   __syncthreads();
   sum = (s_sum[0] + s_sum[1]) + (s_sum[2] + s_sum[3]);
-  long long want = (sum * a.Hkv + target - 1) / target;
-  want = (want + kWarps - 1) / kWarps * kWarps;
-  const int chunk = static_cast<int>(want < kMinBlocks ? kMinBlocks : want);
-  int base = 0, pbase = 0;
-  for (int b0 = 0; b0 < a.B && base <= u; b0 += kThreads) {
+  const int active = static_cast<int>(sum >> 40);
+  sum &= (1LL << 40) - 1;
+  const long long total = sum * a.Hkv;
+  if (total == 0) return;
+  // at least kPairCost + kMinBlocks, but no more than the mean pair: short ones have
+  // a CTA each
+  const long long mean = (sum + active - 1) / active;
+  long long run = (total + gridDim.x - 1) / gridDim.x;
+  const long long least = mean < kPairCost + kMinBlocks ? mean : kPairCost + kMinBlocks;
+  if (run < least) run = least;
+  const long long start = run * blockIdx.x;
+  if (start >= total) return;
+  const long long end = start + run < total ? start + run : total;
+  // the sequence in which it starts, and that one's first block
+  __syncthreads();
+  long long base = 0;
+  for (int b0 = 0; b0 < a.B && base <= start; b0 += kThreads) {
     const int b = b0 + threadIdx.x;
-    const int n = b0 == 0 ? n0 : (b < a.B ? blocks_of(a, b, 8 * NT) : -1);
-    const int nsplit = n < 0 ? 0 : (n <= chunk ? 1 : (n + chunk - 1) / chunk);
-    const int mine = nsplit * a.Hkv, parts = nsplit > 1 ? mine : 0;
-    int incl = mine, pincl = parts;
+    const int w = b0 == 0 ? w0 : static_cast<int>(share(b));
+    long long incl = static_cast<long long>(w) * a.Hkv;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      const int pup = __shfl_up_sync(0xffffffffu, pincl, o);
-      if (lane >= o) {
-        incl += up;
-        pincl += pup;
-      }
+      const long long up = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += up;
     }
-    if (lane == 31) s_scan[warp] = make_int2(incl, pincl);
+    if (lane == 31) s_sum[warp] = incl;
     __syncthreads();
-    int before = base, pbefore = pbase;
+    long long before = base;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) {
-        before += s_scan[w].x;
-        pbefore += s_scan[w].y;
-      }
-      base += s_scan[w].x;
-      pbase += s_scan[w].y;
+    for (int i = 0; i < kWarps; ++i) {
+      if (i < warp) before += s_sum[i];
+      base += s_sum[i];
     }
-    const int off = u - (before + incl - mine);
-    if (off >= 0 && off < mine) {
-      s_unit[0] = b;
-      s_unit[1] = off;
-      s_unit[2] = nsplit;
-      s_unit[3] = pbefore + pincl - parts + off;    // its number among the split ones
+    const long long first = before + incl - static_cast<long long>(w) * a.Hkv;
+    if (start >= first && start < before + incl) {
+      s_b = b;
+      s_start = first;
     }
     __syncthreads();
   }
-  const int b = s_unit[0];
-  if (b < 0) return;
-  const int nsplit = s_unit[2];
-  const int hk = s_unit[1] / nsplit, split = s_unit[1] - hk * nsplit;
-  const RowRange rr = rows_of(a.q_start, b, a.T);
-  const int g = a.g, R = rr.n * g;
-  const int Lb = clamp_len(a.seqlen[b], a.width * a.page);
-  const int nblk = (Lb + 15) >> 4;
-  const int ppb = a.page >> 4;
-  const int blk0 = split * chunk + warp;
-  const int blk1 = (split + 1) * chunk < nblk ? (split + 1) * chunk : nblk;
-  const int niter = blk0 < blk1 ? (blk1 - blk0 + kWarps - 1) / kWarps : 0;
-  const int* table_row = a.table + static_cast<size_t>(b) * a.width;
+  int b = s_b;
+  long long seq0 = s_start;                // the run's position of sequence b's first block
+  long long at = start;
 
-  // --- copies: the numbers of 32 iterations' blocks are looked up at a time, one
-  // a lane; each copy instruction moves 512 contiguous bytes ---
   uint8_t* wring = smem + warp * kStages * kStageBytes;
-  const uint32_t ring0 = smem_u32(wring);
-  const uint32_t s_lo = 16 * chunk_slot(lane), s_hi = 16 * chunk_slot(32 + lane);
-  int window = -1;
-  auto issue = [&](int it) {
-    if (it < niter) {
-      if ((it & 31) == 0) {
-        const int blk = blk0 + (it + lane) * kWarps;
-        window = blk < blk1 ? pool_block(table_row, blk, ppb, a.pages, a.Hkv, hk) : -1;
-      }
-      const int blk = __shfl_sync(0xffffffffu, window, it & 31);
-      if (blk >= 0) {
-        const uint32_t dst = ring0 + (it % kStages) * kStageBytes;
-        const uint8_t* kp = a.kc + static_cast<size_t>(blk) * 1024 + 16 * lane;
-        const uint8_t* vp = a.vc + static_cast<size_t>(blk) * 1024 + 16 * lane;
-        cp_async16(dst + s_lo, kp);
-        cp_async16(dst + s_hi, kp + 512);
-        cp_async16(dst + 1024 + s_lo, vp);
-        cp_async16(dst + 1024 + s_hi, vp + 512);
-        if (lane < 8)
-          cp_async16(dst + 2048 + 16 * lane,
-                     reinterpret_cast<const uint8_t*>(a.sc) + static_cast<size_t>(blk) * 128 +
-                         16 * lane);
-      }
-    }
-    cp_async_commit();   // an empty group past the end keeps the counting uniform
-  };
-#pragma unroll
-  for (int it = 0; it < kStages - 1; ++it) issue(it);
-
-  // --- Q^T as B fragments (k = dimensions, n = row 8 nt + gid) and the sums Q of
-  // the rows 8 nt + 2 tig + c of this lane's accumulators ---
-  uint32_t qb[NT][8][2];
-  float qh[NT][2];
-  int lim[NT][2];          // tokens a row sees
+  const uint32_t ring_lo = smem_u32(wring) + 16 * chunk_slot(lane);
+  const uint32_t ring_hi = smem_u32(wring) + 16 * chunk_slot(32 + lane);
+  const uint32_t ring_sc = smem_u32(wring) + 2048 + 16 * lane;
+  const uint8_t* k_lane = a.kc + 16 * lane;
+  const uint8_t* v_lane = a.vc + 16 * lane;
+  const uint8_t* s_lane = reinterpret_cast<const uint8_t*>(a.sc) + 16 * (lane & 7);
+  const int ppb = a.page >> 4, g = a.g;
   const float scale2 = a.scale * 1.4426950408889634f;   // scores in log2 units
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + gid;
-    const bool ok = r < R;
-    const int qi = r / g;
-    const __half* q = a.Q + static_cast<size_t>(rr.first + (ok ? qi : 0)) * a.ldq +
-                      static_cast<size_t>(hk * g + (ok ? r - qi * g : 0)) * kHeadDim;
-    float qs = 0.0f;
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      const int d0 = 16 * ks + 2 * tig;
-      qb[nt][ks][0] = ok ? *reinterpret_cast<const uint32_t*>(q + d0) : 0u;
-      qb[nt][ks][1] = ok ? *reinterpret_cast<const uint32_t*>(q + d0 + 8) : 0u;
-      const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&qb[nt][ks][0]));
-      const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&qb[nt][ks][1]));
-      qs += (f0.x + f0.y) + (f1.x + f1.y);
-    }
-    qs += __shfl_xor_sync(0xffffffffu, qs, 1);
-    qs += __shfl_xor_sync(0xffffffffu, qs, 2);
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      qh[nt][c] = __shfl_sync(0xffffffffu, qs, 8 * tig + 4 * c) * scale2;
-      const int row = 8 * nt + 2 * tig + c;
-      lim[nt][c] = row < R ? visible(position_of(a.seqlen[b], rr.n, row / g), Lb) : 0;
-    }
-  }
-  const int all_see = visible(position_of(a.seqlen[b], rr.n, 0), Lb);
 
-  float acc[NT][8][4];
-  float mrun[NT][2], lsum[NT][2], osum[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int mt = 0; mt < 8; ++mt)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[nt][mt][k] = 0.0f;
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      mrun[nt][c] = -INFINITY;
-      lsum[nt][c] = osum[nt][c] = 0.0f;
+  while (at < end) {
+    // --- the next pair: KV head hk of sequence b, and its blocks [c0, c1) ---
+    const int nblk = blocks_of(a, b, kRows), weight = weight_of(nblk);
+    if (at >= seq0 + static_cast<long long>(weight) * a.Hkv) {
+      seq0 += static_cast<long long>(weight) * a.Hkv;
+      ++b;
+      continue;
     }
-  }
+    const int into = static_cast<int>(at - seq0);
+    const int hk = into / weight, from = into - hk * weight;
+    const long long left = end - at;
+    const int to = weight - from < left ? weight : from + static_cast<int>(left);
+    at += to - from;
+    const int c0 = from < kPairCost ? 0 : from - kPairCost, c1 = to - kPairCost;
+    if (c1 <= 0) continue;      // the run ends before the pair's first block
+    const bool whole = c0 == 0 && to == weight;
+    const RowRange rr = rows_of(a.q_start, b, a.T);
+    const int R = rr.n * g;
+    const int seqlen = a.seqlen[b], Lb = clamp_len(seqlen, a.width * a.page);
+    const int blk0 = c0 + 2 * warp, blk1 = c1 < nblk ? c1 : nblk;
+    const int niter = blk0 < blk1 ? (blk1 - blk0 + 2 * kWarps - 1) / (2 * kWarps) : 0;
+    const int* table_row = a.table + static_cast<size_t>(b) * a.width;
 
-  uint32_t absent = 0;    // of 32 iterations: the blocks whose page is not in the pool
-  for (int it = 0; it < niter; ++it) {
-    cp_async_wait<kStages - 2>();
-    __syncwarp();
-    // (the copies run less than 32 iterations ahead: at a multiple of 32 the
-    // window is still the one of this iteration)
-    if ((it & 31) == 0) absent = __ballot_sync(0xffffffffu, window < 0);
-    const int blk = blk0 + it * kWarps;
-    const uint8_t* stage = wring + (it % kStages) * kStageBytes;
-    const uint4 kq0 = *reinterpret_cast<const uint4*>(stage + 16 * chunk_slot(2 * lane));
-    const uint4 kq1 = *reinterpret_cast<const uint4*>(stage + 16 * chunk_slot(2 * lane + 1));
-    const uint4 vq0 = *reinterpret_cast<const uint4*>(stage + 1024 + 16 * chunk_slot(2 * lane));
-    const uint4 vq1 = *reinterpret_cast<const uint4*>(stage + 1024 + 16 * chunk_slot(2 * lane + 1));
-    const uint2 sq[2] = {*reinterpret_cast<const uint2*>(stage + 2048 + 8 * gid),
-                         *reinterpret_cast<const uint2*>(stage + 2048 + 64 + 8 * gid)};
-    __syncwarp();           // every lane has read the stage before it is copied into again
-    issue(it + kStages - 1);
-    if ((absent >> (it & 31)) & 1u) continue;
-
-    auto step = [&](auto masked) {
-      constexpr bool kMasked = decltype(masked)::value;
-      const uint32_t wk[8] = {kq0.x, kq0.y, kq0.z, kq0.w, kq1.x, kq1.y, kq1.z, kq1.w};
-      const uint32_t wv[8] = {vq0.x, vq0.y, vq0.z, vq0.w, vq1.x, vq1.y, vq1.z, vq1.w};
-      // S^T = C_K Q^T: rows tokens gid and gid + 8, columns rows 2 tig and + 1
-      float s[NT][4], s2[NT][4];
+    // --- copies: the numbers of 16 iterations' block pairs are looked up at a
+    // time, one block a lane; each copy instruction moves 512 contiguous bytes ---
+    int window = -1;
+    auto issue = [&](int it) {
+      if (it < niter) {
+        if ((it & 15) == 0) {
+          const int blk = blk0 + (it + (lane >> 1)) * (2 * kWarps) + (lane & 1);
+          window = blk < blk1 ? pool_block(table_row, blk, ppb, a.pages, a.Hkv, hk) : -1;
+        }
+        const uint32_t stage = (it & (kStages - 1)) * kStageBytes;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) s[nt][k] = s2[nt][k] = 0.0f;
-#pragma unroll
-      for (int ks = 0; ks < 8; ks += 2) {
-        uint32_t f0[4], f1[4];
-        a_frag(wk[ks], f0);
-        a_frag(wk[ks + 1], f1);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_16816(s[nt], f0, qb[nt][ks][0], qb[nt][ks][1]);
-          mma_16816(s2[nt], f1, qb[nt][ks + 1][0], qb[nt][ks + 1][1]);
+        for (int i = 0; i < 2; ++i) {
+          const int blk = __shfl_sync(0xffffffffu, window, 2 * (it & 15) + i);
+          if (blk >= 0) {
+            const size_t off = static_cast<size_t>(static_cast<uint32_t>(blk)) * 1024u;
+            const uint32_t lo = ring_lo + stage + i * kBlockBytes;
+            const uint32_t hi = ring_hi + stage + i * kBlockBytes;
+            cp_async16(lo, k_lane + off);
+            cp_async16(hi, k_lane + off + 512);
+            cp_async16(lo + 1024, v_lane + off);
+            cp_async16(hi + 1024, v_lane + off + 512);
+            if (lane < 8)
+              cp_async16(ring_sc + stage + i * kBlockBytes,
+                         s_lane + static_cast<size_t>(static_cast<uint32_t>(blk)) * 128u);
+          }
         }
       }
-      float skt[2], mkt[2], svt[2], mvt[2];
+      cp_async_commit();   // an empty group past the end keeps the counting uniform
+    };
+    static_assert((kStages & (kStages - 1)) == 0, "ring index");
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float2 k2 = __half22float2(*reinterpret_cast<const __half2*>(&sq[r].x));
-        const float2 v2 = __half22float2(*reinterpret_cast<const __half2*>(&sq[r].y));
-        skt[r] = k2.x * ((r ? kRowScale1 : kRowScale0) * scale2);
-        mkt[r] = k2.y;
-        svt[r] = v2.x;
-        mvt[r] = v2.y;
-      }
-      bool raise = false;
-      float x[NT][4];
+    for (int it = 0; it < kStages - 1; ++it) issue(it);
+
+    // --- queries as B fragments: column gid is row 4 nt + gid / 2, its high byte
+    // (even) or low byte (odd); bytes are dimensions 2 tig + {0, 8, 1, 9} of words
+    // 2 ks and 2 ks + 1, as the codes' ---
+    uint32_t qb[NT][4][2];
+    float qf[NT], qh[NT];    // of row 4 nt + tig: the fixed point's unit and Q, in score units
+    int lim[NT];             // tokens it sees
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 4 * nt + (gid >> 1);
+      const bool ok = r < R;
+      const int qi = r / g;
+      const __half* q = a.Q + static_cast<size_t>(rr.first + (ok ? qi : 0)) * a.ldq +
+                        static_cast<size_t>(hk * g + (ok ? r - qi * g : 0)) * kHeadDim + 2 * tig;
+      float2 f[4][4];
+      float qs = 0.0f, top = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = k >> 1, c = k & 1;
-          s[nt][k] += s2[nt][k];
-          // relative to the running maximum (-inf at first: the sum is then no
-          // number below the threshold)
-          float v = fmaf(skt[r], s[nt][k], fmaf(mkt[r], qh[nt][c], -mrun[nt][c]));
-          if (kMasked && blk * 16 + gid + 8 * r >= lim[nt][c]) v = -INFINITY;
-          x[nt][k] = v;
-          raise |= !(v <= kRaise);
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[ks][i] = ok ? __half22float2(*reinterpret_cast<const __half2*>(q + 32 * ks + 8 * i))
+                        : make_float2(0.0f, 0.0f);
+          qs += f[ks][i].x + f[ks][i].y;
+          top = fmaxf(top, fmaxf(fabsf(f[ks][i].x), fabsf(f[ks][i].y)));
         }
-      if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int o = 1; o < 4; o <<= 1) {
+        qs += __shfl_xor_sync(0xffffffffu, qs, o);
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      }
+      const float up = top > 0.0f ? kFixed / top : 0.0f;
+      auto byte = [&](float v) {
+        const int n = __float2int_rn(v * up);
+        const int h = (n + 128) >> 8;
+        return static_cast<uint32_t>((gid & 1) ? n - 256 * h : h) & 0xffu;
+      };
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float y[2];
+      for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const float2 p = f[ks][2 * w], o = f[ks][2 * w + 1];
+          qb[nt][ks][w] = byte(p.x) | byte(o.x) << 8 | byte(p.y) << 16 | byte(o.y) << 24;
+        }
+      qf[nt] = __shfl_sync(0xffffffffu, top, 8 * tig) * (scale2 / kFixed);
+      qh[nt] = __shfl_sync(0xffffffffu, qs, 8 * tig) * scale2;
+      const int row = 4 * nt + tig;
+      lim[nt] = row < R ? visible(position_of(seqlen, rr.n, row / g), Lb) : 0;
+    }
+    const int all_see = visible(position_of(seqlen, rr.n, 0), Lb);
+
+    float acc[NT][8][4];     // dimensions 16 mt + gid and + 8, the weights' high and low parts
+    float mrun[NT], lsum[NT], osum[NT];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[nt][mt][k] = 0.0f;
+      mrun[nt] = -INFINITY;
+      lsum[nt] = osum[nt] = 0.0f;
+    }
+
+    uint32_t absent = 0;    // of 16 iterations: the blocks whose page is not in the pool
+    for (int it = 0; it < niter; ++it) {
+      cp_async_wait<kStages - 2>();
+      __syncwarp();
+      // (the copies run less than 16 iterations ahead: at a multiple of 16 the
+      // window is still the one of this iteration)
+      if ((it & 15) == 0) absent = __ballot_sync(0xffffffffu, window < 0);
+      issue(it + kStages - 1);
+      const int blk = blk0 + it * (2 * kWarps);
+      const uint32_t gone = (absent >> (2 * (it & 15))) & 3u;
+      const uint8_t* stage = wring + (it & (kStages - 1)) * kStageBytes;
+
+      auto step = [&](auto masked) {
+        constexpr bool kMasked = decltype(masked)::value;
+        // scores of tokens gid and gid + 8 of block i with row 4 nt + tig, in units of
+        // the fixed point
+        float s[2][NT][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* kp = stage + i * kBlockBytes;
+          const uint4 k0 = *reinterpret_cast<const uint4*>(kp + 16 * chunk_slot(2 * lane));
+          const uint4 k1 = *reinterpret_cast<const uint4*>(kp + 16 * chunk_slot(2 * lane + 1));
+          const uint32_t wk[8] = {k0.x, k0.y, k0.z, k0.w, k1.x, k1.y, k1.z, k1.w};
+          int d[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) d[nt][k] = 0;
+#pragma unroll
+          for (int ks = 0; ks < 4; ++ks) {
+            const uint32_t a0 = wk[2 * ks] & 0x0f0f0f0fu, a1 = (wk[2 * ks] >> 4) & 0x0f0f0f0fu;
+            const uint32_t a2 = wk[2 * ks + 1] & 0x0f0f0f0fu;
+            const uint32_t a3 = (wk[2 * ks + 1] >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_u8s8(d[nt], a0, a1, a2, a3, qb[nt][ks][0], qb[nt][ks][1]);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            s[i][nt][0] = __int2float_rn(256 * d[nt][0] + d[nt][1]);
+            s[i][nt][1] = __int2float_rn(256 * d[nt][2] + d[nt][3]);
+          }
+        }
+        float skt[2][2], mkt[2][2], svt[2][2], mvt[2][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const uint2 sq = *reinterpret_cast<const uint2*>(stage + i * kBlockBytes + 2048 +
+                                                             64 * r + 8 * gid);
+            const float2 k2 = __half22float2(*reinterpret_cast<const __half2*>(&sq.x));
+            const float2 v2 = __half22float2(*reinterpret_cast<const __half2*>(&sq.y));
+            skt[i][r] = k2.x;
+            mkt[i][r] = k2.y;
+            svt[i][r] = v2.x;
+            mvt[i][r] = fmaf(8.0f, v2.x, v2.y);
+          }
+        auto hidden = [&](int i, int r, int nt) {
+          return kMasked && ((blk + i) * 16 + gid + 8 * r >= lim[nt] || ((gone >> i) & 1u));
+        };
+        bool raise = false;
+        float x[2][NT][2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              y[r] = fmaf(skt[r], s[nt][2 * r + c], mkt[r] * qh[nt][c]);
-              if (kMasked && blk * 16 + gid + 8 * r >= lim[nt][c]) y[r] = -INFINITY;
+              // relative to the running maximum (-inf at first: the sum is then no
+              // number below the threshold)
+              float v = fmaf(skt[i][r] * qf[nt], s[i][nt][r], fmaf(mkt[i][r], qh[nt], -mrun[nt]));
+              if (hidden(i, r, nt)) v = -INFINITY;
+              x[i][nt][r] = v;
+              raise |= !(v <= kRaise);
             }
-            float top = fmaxf(y[0], y[1]);
+        if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float y[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                y[i][r] = fmaf(skt[i][r] * qf[nt], s[i][nt][r], mkt[i][r] * qh[nt]);
+                if (hidden(i, r, nt)) y[i][r] = -INFINITY;
+              }
+            float top = fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[1][0], y[1][1]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, mrun[nt][c]);
-            const float al = top == -INFINITY ? 1.0f : fast_exp2(mrun[nt][c] - top);
-            mrun[nt][c] = top;
-            lsum[nt][c] *= al;
-            osum[nt][c] *= al;
+            top = fmaxf(top, mrun[nt]);
+            const float al = top == -INFINITY ? 1.0f : fast_exp2(mrun[nt] - top);
+            mrun[nt] = top;
+            lsum[nt] *= al;
+            osum[nt] *= al;
 #pragma unroll
-            for (int mt = 0; mt < 8; ++mt) {
-              acc[nt][mt][c] *= al;
-              acc[nt][mt][2 + c] *= al;
-            }
+            for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) acc[nt][mt][k] *= al;
             const float ref = top == -INFINITY ? 0.0f : top;
-            x[nt][c] = y[0] - ref;
-            x[nt][2 + c] = y[1] - ref;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              x[i][nt][0] = y[i][0] - ref;
+              x[i][nt][1] = y[i][1] - ref;
+            }
           }
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float wt[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = k >> 1, c = k & 1;
-          const float p = fast_exp2(x[nt][k]);
-          lsum[nt][c] += p;
-          // (a masked token's scales may never have been written: its terms are
-          // left out, not multiplied by 0)
-          const bool in = !kMasked || x[nt][k] != -INFINITY;
-          wt[k] = in ? p * svt[r] : 0.0f;
-          osum[nt][c] += in ? p * mvt[r] : 0.0f;
         }
-        const uint32_t top = pack_h2(wt[0], wt[1]), bot = pack_h2(wt[2], wt[3]);
-        const float2 ft = __half22float2(*reinterpret_cast<const __half2*>(&top));
-        const float2 fb = __half22float2(*reinterpret_cast<const __half2*>(&bot));
-        osum[nt][0] = fmaf(8.0f, (wt[0] - ft.x) + (wt[2] - fb.x), osum[nt][0]);
-        osum[nt][1] = fmaf(8.0f, (wt[1] - ft.y) + (wt[3] - fb.y), osum[nt][1]);
-        const uint32_t b0 = transpose8x8(top), b1 = transpose8x8(bot);
-        // O^T += C_V^T W^T, dimensions 16 mt .. from word mt
+        uint32_t wb[2][NT][2];     // W^T as B fragments: k = tokens of block i
 #pragma unroll
-        for (int mt = 0; mt < 8; ++mt) {
-          uint32_t f[4];
-          a_frag(wv[mt], f);
-          mma_16816(acc[nt][mt], f, b0, b1);
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float p = fast_exp2(x[i][nt][r]);
+              lsum[nt] += p;
+              // (a hidden token's scales may never have been written: its terms are
+              // left out, not multiplied by 0)
+              const bool in = !kMasked || x[i][nt][r] != -INFINITY;
+              const float w = in ? p * svt[i][r] : 0.0f;
+              if (in) osum[nt] = fmaf(p, mvt[i][r], osum[nt]);
+              const float high = __half2float(__float2half_rn(w));
+              wb[i][nt][r] = transpose8x8(pack_h2(high, w - high));
+            }
+        // O^T += (C_V - 8)^T W^T, dimensions 16 mt .. from word mt
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint8_t* vp = stage + i * kBlockBytes + 1024;
+          const uint4 v0 = *reinterpret_cast<const uint4*>(vp + 16 * chunk_slot(2 * lane));
+          const uint4 v1 = *reinterpret_cast<const uint4*>(vp + 16 * chunk_slot(2 * lane + 1));
+          const uint32_t wv[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) {
+            uint32_t f[4];
+            v_frag(wv[mt], f);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(acc[nt][mt], f, wb[i][nt][0], wb[i][nt][1]);
+          }
         }
-      }
-    };
-    if (blk * 16 + 16 <= all_see) step(std::false_type{});
-    else step(std::true_type{});
-  }
-  cp_async_wait<0>();
-  __syncthreads();   // the ring becomes the merge area
+      };
+      if ((blk + 2) * 16 <= all_see && gone == 0u) step(std::false_type{});
+      else step(std::true_type{});
+      __syncwarp();           // every lane has read the stage before it is copied into again
+    }
+    cp_async_wait<0>();
+    __syncthreads();   // the ring becomes the merge area
 
-  // per warp and row: max, sum, 128 outputs
-  float* mrg = reinterpret_cast<float*>(smem);     // [warp][8 NT][kPartFloats]
-  static_assert(sizeof(float) * kWarps * 8 * NT * kPartFloats <= sizeof(smem), "merge area");
+    // per warp and row: max, sum, 128 outputs
+    float* mrg = reinterpret_cast<float*>(smem);     // [warp][kRows][kPartFloats]
+    static_assert(sizeof(float) * kRows * kPartFloats <= kStages * kStageBytes, "merge area");
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      float l = lsum[nt][c], o = osum[nt][c];
+    for (int nt = 0; nt < NT; ++nt) {
+      float l = lsum[nt], o = osum[nt];
 #pragma unroll
       for (int d = 4; d < 32; d <<= 1) {
         l += __shfl_xor_sync(0xffffffffu, l, d);
         o += __shfl_xor_sync(0xffffffffu, o, d);
       }
-      float* row = mrg + (warp * 8 * NT + 8 * nt + 2 * tig + c) * kPartFloats;
+      float* row = mrg + (warp * kRows + 4 * nt + tig) * kPartFloats;
       if (gid == 0) {
-        row[0] = mrun[nt][c];
+        row[0] = mrun[nt];
         row[1] = l;
       }
 #pragma unroll
       for (int mt = 0; mt < 8; ++mt) {
-        row[4 + 16 * mt + gid] = fmaf(acc[nt][mt][c], kRowScale0, o);
-        row[4 + 16 * mt + gid + 8] = fmaf(acc[nt][mt][2 + c], kRowScale1, o);
+        row[4 + 16 * mt + gid] = acc[nt][mt][0] + acc[nt][mt][1] + o;
+        row[4 + 16 * mt + gid + 8] = acc[nt][mt][2] + acc[nt][mt][3] + o;
       }
     }
-  __syncthreads();
-  const int pair = b * a.Hkv + hk;
-  if (threadIdx.x == 0 && split == 0 && a.meta != nullptr)
-    a.meta[pair] = make_int2(s_unit[3], nsplit);
-  // 16 threads a row, 8 dimensions each
-  const int d0 = 8 * (threadIdx.x & 15);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = 8 * nt + (threadIdx.x >> 4);
-    if (r >= R) continue;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mrg[(w * 8 * NT + r) * kPartFloats]);
-    float den = 0.0f, v[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float* row = mrg + (w * 8 * NT + r) * kPartFloats;
-      const float f = row[0] == -INFINITY ? 0.0f : fast_exp2(row[0] - M);
-      if (f == 0.0f) continue;
-      den += f * row[1];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] += f * row[4 + d0 + k];
+    __syncthreads();
+    if (threadIdx.x == 0 && c0 == 0 && a.meta != nullptr) {
+      // the CTAs that hold the pair's first and last block
+      const long long last = seq0 + static_cast<long long>(hk + 1) * weight - 1;
+      a.meta[b * a.Hkv + hk] = make_int2(static_cast<int>(blockIdx.x), static_cast<int>(last / run));
     }
-    if (nsplit == 1) {
-      const int qi = r / g;
-      const float inv = den > 0.0f ? __frcp_rn(den) : 0.0f;
-      if (!(den > 0.0f) && den == den)
+    // a warp a row at a time, four dimensions a lane
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = 0.0f;
-      store_row8(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * g + (r - qi * g)) *
-                             kHeadDim + d0, v, den == den ? inv : den);
-    } else {
-      float* part = a.parts + (static_cast<size_t>(s_unit[3]) * (8 * NT) + r) * kPartFloats;
-      if ((threadIdx.x & 15) == 0) {
-        part[0] = M;
-        part[1] = den;
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 4 * nt + warp;
+      if (r >= R) continue;
+      float M = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, mrg[(w * kRows + r) * kPartFloats]);
+      float den = 0.0f;
+      float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float* row = mrg + (w * kRows + r) * kPartFloats;
+        const float f = row[0] == -INFINITY ? 0.0f : fast_exp2(row[0] - M);
+        if (f == 0.0f) continue;
+        den += f * row[1];
+        const float4 o = *reinterpret_cast<const float4*>(row + 4 + 4 * lane);
+        v.x += f * o.x;
+        v.y += f * o.y;
+        v.z += f * o.z;
+        v.w += f * o.w;
       }
-      *reinterpret_cast<float4*>(part + 4 + d0) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(part + 8 + d0) = make_float4(v[4], v[5], v[6], v[7]);
+      if (whole) {
+        // (v is 0 where the row saw no token)
+        const int qi = r / g;
+        store_row4(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * g + (r - qi * g)) *
+                               kHeadDim + 4 * lane, v, den == 0.0f ? 0.0f : __frcp_rn(den));
+      } else {
+        float* part = a.parts + (static_cast<size_t>(2 * blockIdx.x + (c0 == 0 ? 1 : 0)) * kRows +
+                                 r) * kPartFloats;
+        if (lane == 0) {
+          part[0] = M;
+          part[1] = den;
+        }
+        *reinterpret_cast<float4*>(part + 4 + 4 * lane) = v;
+      }
     }
+    __syncthreads();   // the merge area becomes the ring again
   }
 }
 
@@ -455,20 +534,23 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a, i
       rr = rows_of(a.q_start, b, a.T);
       if (r < rr.n * a.g) {
         mt = a.meta[pair];
-        n = mt.y > 1 ? mt.y : 0;
+        n = mt.y > mt.x ? mt.y - mt.x + 1 : 0;   // CTAs that hold a part of it
       }
     }
   }
-  const float* base = a.parts + (static_cast<size_t>(mt.x) * stride + r) * kPartFloats;
+  // the first part is at its CTA's end (place 2 x + 1), the others at their CTAs'
+  // beginnings (places 2 (x + p))
+  const float* base = a.parts + (static_cast<size_t>(2 * mt.x) * stride + r) * kPartFloats;
   const size_t step = static_cast<size_t>(stride) * kPartFloats;
+  auto part = [&](int p) { return base + (p == 0 ? step : 2 * p * step); };
   float M = -INFINITY, den = 0.0f;
   float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int p = lane; p < n; p += 32) M = fmaxf(M, base[p * step]);
+  for (int p = lane; p < n; p += 32) M = fmaxf(M, part(p)[0]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
 #pragma unroll 4
   for (int p = sub; p < n; p += W) {
-    const float* pp = base + p * step;
+    const float* pp = part(p);
     const float m = pp[0];
     const float f = m == -INFINITY ? 0.0f : fast_exp2(m - M);
     const float4 v = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
@@ -494,29 +576,29 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a, i
     }
   }
   if (n == 0) return;
-  const float inv = den == 0.0f ? 0.0f : __frcp_rn(den);
   const int qi = r / a.g;
-  __half2 o[2] = {__floats2half2_rn(num.x * inv, num.y * inv),
-                  __floats2half2_rn(num.z * inv, num.w * inv)};
-  *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g +
-                                     (r - qi * a.g)) * kHeadDim + 4 * lane) =
-      *reinterpret_cast<const uint2*>(o);
+  store_row4(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g + (r - qi * a.g)) *
+                         kHeadDim + 4 * lane, num, den == 0.0f ? 0.0f : __frcp_rn(den));
 }
 
 template <int NT>
 int launch_decode(const PagedArgs& a, const PagedPlan& p, cudaStream_t s) {
+  constexpr size_t smem = static_cast<size_t>(kWarps) * kStages * kStageBytes;
+  static std::atomic<unsigned long long> ready{0};
+  if (int st = opt_in_smem(reinterpret_cast<const void*>(paged_decode_kernel<NT>), smem, ready))
+    return st;
   if (int st = launch_dependent(paged_decode_kernel<NT>, dim3(static_cast<unsigned>(p.grid)),
-                                kThreads, 0, s, a, p.target))
+                                kThreads, smem, s, a))
     return st;
   if (!p.combine) return QOQ_OK;
-  const int rows = a.max_q * a.g < 8 * NT ? a.max_q * a.g : 8 * NT;
+  const int rows = a.max_q * a.g < 4 * NT ? a.max_q * a.g : 4 * NT;
   const long long all = static_cast<long long>(a.B) * a.Hkv * rows;
-  // few rows have many splits each: eight warps a row
+  // few rows have many parts each: eight warps a row
   if (all <= 512)
     return launch_dependent(paged_combine_kernel<8>, dim3(static_cast<unsigned>(all)), 256, 0, s, a,
-                            rows, 8 * NT);
+                            rows, 4 * NT);
   return launch_dependent(paged_combine_kernel<1>, dim3(static_cast<unsigned>((all + 7) / 8)), 256,
-                          0, s, a, rows, 8 * NT);
+                          0, s, a, rows, 4 * NT);
 }
 
 }  // namespace
@@ -526,24 +608,19 @@ PagedPlan paged_plan(int T, int B, int Hq, int Hkv, int width, int page, int max
   const int g = Hq / Hkv;
   const long long pairs = static_cast<long long>(B) * Hkv;
   const long long most = static_cast<long long>(max_q) * g;     // rows of a sequence
-  p.nt = most <= 8 || g <= 8 ? 1 : (g <= 16 ? 2 : 0);
-  if (most > 8 && most <= 16) p.nt = 2;
-  p.prompt = most > 8 * p.nt;
+  // tiles of four rows: for all sequences, or, where there are longer ones (prompt
+  // chunks), for those with one query token
+  p.nt = most <= 4 ? 1 : (most <= 8 ? 2 : (most <= 16 ? 4 : (g <= 4 ? 1 : (g <= 8 ? 2 : (g <= 16 ? 4 : 0)))));
+  p.prompt = most > 4 * p.nt;
   const long long blocks = (static_cast<long long>(width) * page + 15) / 16;
   if (p.nt) {
-    const long long most_splits = (blocks + kMinBlocks - 1) / kMinBlocks;
-    p.target = 8 * sm_count();
-    const long long a = p.target + pairs, b = pairs * most_splits;
-    p.grid = static_cast<int>(a < b ? a : b);
-    p.combine = most_splits > 1;
+    // a CTA for each that is resident, but no more than there can be blocks
+    const int resident = resident_ctas(p.nt) * sm_count();
+    p.grid = static_cast<int>(pairs * blocks < resident ? pairs * blocks : resident);
+    p.combine = p.grid > 1;
     if (p.combine) {
-      // A sequence is split where its length n is over chunk >= blocks * Hkv / target
-      // (all in blocks), into fewer than n / chunk + 1 < 2 n / chunk: at most 2 target
-      // units of the batch leave partial results.
-      const long long split = 2LL * p.target;
-      const long long parts = split < p.grid ? split : p.grid;
       p.meta_off = p.take(static_cast<size_t>(pairs) * sizeof(int2));
-      p.parts_off = p.take(static_cast<size_t>(parts) * 8 * p.nt * kPartFloats * sizeof(float));
+      p.parts_off = p.take(static_cast<size_t>(2 * p.grid) * 4 * p.nt * kPartFloats * sizeof(float));
     }
   }
   if (p.prompt) plan_prompt(p, T, B, Hq, Hkv, width, page);
@@ -615,13 +692,14 @@ extern "C" int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq,
   if (p.nt) {
     a.meta = p.combine ? reinterpret_cast<int2*>(w + p.meta_off) : nullptr;
     a.parts = p.combine ? reinterpret_cast<float*>(w + p.parts_off) : nullptr;
-    const int st = p.nt == 1 ? launch_decode<1>(a, p, s) : launch_decode<2>(a, p, s);
+    const int st = p.nt == 1 ? launch_decode<1>(a, p, s)
+                             : (p.nt == 2 ? launch_decode<2>(a, p, s) : launch_decode<4>(a, p, s));
     if (st) return st;
   }
   if (p.prompt) {
     a.meta = p.prompt_combine ? reinterpret_cast<int2*>(w + p.prompt_meta_off) : nullptr;
     a.parts = p.prompt_combine ? reinterpret_cast<float*>(w + p.prompt_parts_off) : nullptr;
-    return launch_paged_prompt(a, p, 8 * p.nt + 1, s);
+    return launch_paged_prompt(a, p, 4 * p.nt + 1, s);
   }
   return QOQ_OK;
 }

@@ -192,7 +192,7 @@ __device__ __forceinline__ float4 lds16(uint32_t at) {
 // Nibbles 4 s and 4 s + 16 of a word as FP16 numbers c - 8 (0x6400 | c is
 // 1024 + c).
 __device__ __forceinline__ uint32_t centred(uint32_t word, int s) {
-  const uint32_t n = ((word >> s) & 0x000f000fu) | 0x64006400u;
+  const uint32_t n = and_or(word >> s, 0x000f000fu, 0x64006400u);
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&n), __float2half2_rn(1032.0f));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
@@ -745,41 +745,17 @@ paged_prompt_combine_kernel(const PagedArgs a, int tiles, int min_rows) {
     num.z += f * v.z;
     num.w += f * v.w;
   }
-  const float inv = den == 0.0f ? 0.0f : __frcp_rn(den);
   const int qi = r / a.g;
-  __half2 o[2] = {__floats2half2_rn(num.x * inv, num.y * inv),
-                  __floats2half2_rn(num.z * inv, num.w * inv)};
-  *reinterpret_cast<uint2*>(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g +
-                                     (r - qi * a.g)) * kHeadDim + 4 * lane) =
-      *reinterpret_cast<const uint2*>(o);
+  store_row4(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g + (r - qi * a.g)) *
+                         kHeadDim + 4 * lane, num, den == 0.0f ? 0.0f : __frcp_rn(den));
 }
-
-}  // namespace
-
-namespace {
 
 // Once per device: opt in to the shared memory, and check the registers.  The
 // kernel's warpgroups split 4 x 128 a thread among them (192, 192, 96, 32); a
 // launch with fewer would wait for registers that never come free.
 int prepare_prompt_kernel() {
   static std::atomic<unsigned long long> ready{0};
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) {
-    cudaGetLastError();
-    return QOQ_ERR_CUDA;
-  }
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
-  if (ready.load(std::memory_order_relaxed) & bit) return QOQ_OK;
-  cudaFuncAttributes attr;
-  if (cudaFuncGetAttributes(&attr, paged_prompt_kernel) != cudaSuccess ||
-      cudaFuncSetAttribute(paged_prompt_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(kSmemBytes)) != cudaSuccess) {
-    cudaGetLastError();
-    return QOQ_ERR_CUDA;
-  }
-  if (attr.numRegs < 128) return QOQ_ERR_UNSUPPORTED;
-  ready.fetch_or(bit, std::memory_order_relaxed);
-  return QOQ_OK;
+  return opt_in_smem(reinterpret_cast<const void*>(paged_prompt_kernel), kSmemBytes, ready, 128);
 }
 
 }  // namespace
@@ -791,7 +767,8 @@ void plan_prompt(PagedPlan& p, int T, int B, int Hq, int Hkv, int width, int pag
   const long long pairs = static_cast<long long>(p.tiles) * Hkv;
   const long long steps = (static_cast<long long>(width) * page + kTile - 1) / kTile;
   const long long most_splits = (steps + kMinChunk - 1) / kMinChunk;
-  // (see paged_plan for the bound on the split units)
+  // (split slots have over `chunk` >= steps * Hkv / target steps each, so fewer than
+  // n / chunk + 1 < 2 n / chunk units, and the batch at most 2 target of them)
   const long long units = p.prompt_target + pairs, all = pairs * most_splits;
   p.prompt_grid = static_cast<int>(units < all ? units : all);
   if (most_splits > 1) {
