@@ -543,9 +543,9 @@ QOQ_API int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq, in
  *   out[t] = fp16(Y[t] + scaling[a] * B_a . (A_a . x_t)),   a = ids[t],
  * and out[t] = Y[t] where ids[t] is outside [0, n).
  *   X [T][K], Y, out [T][N] FP16 (out may be Y); A [n][R][K], B [n][N][R] FP16;
- *   ids int32 [T] (any order; runs of one adapter are quicker); scaling FP32
+ *   ids int32 [T] (any order: rows are taken by adapter); scaling FP32
  *   [n].  N % 128 == 0, K % 128 == 0, R % 8 == 0, R <= 128 (adapters of smaller
- *   rank: zeros), T <= 2^20; T = 0 is a call with nothing to do.
+ *   rank: zeros), n <= 4096, T <= 2^20; T = 0 is a call with nothing to do.
  *   ws: at least qoq_lora_workspace_bytes, 16-byte aligned (no zeroing needed),
  *   QOQ_ERR_WORKSPACE otherwise; calls that can run at the same time need
  *   different workspaces.

@@ -88,6 +88,9 @@ CASES = [
     (513, 512, 256, 64, 6, "runs"),
     (700, 256, 384, 128, 40, "random"),
     (1000, 384, 128, 8, 1, "one"),
+    (4200, 128, 128, 16, 300, "random"),       # rows are taken by adapter within 4096
+    (9000, 128, 128, 8, 5, "runs"),
+    (65, 256, 128, 112, 4096, "distinct"),
 ]
 
 

@@ -25,7 +25,8 @@ def test_refusals(L):
         assert _add(L, **{name: odd}) == qoq.QOQ_ERR_INVALID_ARG, name
     for bad in (dict(T=-1), dict(K=0), dict(K=200), dict(N=0), dict(N=100), dict(R=0), dict(n=0)):
         assert _add(L, **bad) == qoq.QOQ_ERR_INVALID_ARG, bad
-    for bad in (dict(R=12), dict(R=136), dict(K=133248), dict(T=(1 << 20) + 1)):
+    for bad in (dict(R=12), dict(R=136), dict(K=133248), dict(T=(1 << 20) + 1),
+                dict(n=4097)):
         assert _add(L, **bad) == qoq.QOQ_ERR_UNSUPPORTED, bad
     need = L.qoq_lora_workspace_bytes(3, 256, 128, 16, 2)
     for bad in (dict(ws=None), dict(ws=ctypes.c_void_p(0x10008)), dict(ws_bytes=need - 1)):
@@ -36,6 +37,8 @@ def test_refusals(L):
 def test_workspace(L):
     f = L.qoq_lora_workspace_bytes
     assert f(0, 256, 128, 16, 2) == 0 and f(4, 200, 128, 16, 2) == 0
-    for T, K, R, n in ((1, 128, 8, 1), (48, 8192, 32, 64), (2500, 14336, 64, 6), (1 << 20, 256, 128, 3)):
+    for T, K, R, n in ((1, 128, 8, 1), (48, 8192, 32, 64), (2500, 14336, 64, 6),
+                       (1 << 20, 256, 128, 3), (4096, 256, 128, 4096)):
         need = f(T, K, 128, R, n)
-        assert need % (T * R * 4) == 0 and 1 <= need // (T * R * 4) <= 16
+        # h in two FP16 parts and a factor a row, a row list a unit
+        assert T * (4 * R + 4) <= need <= T * (4 * (R + 31) + 4) + (T + 256) * 264 + 1024
