@@ -709,45 +709,50 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
   if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-// Rows of the split slots from their partial results, a warp a row.
+// Rows of the split slots from their partial results: kCombineRows rows a CTA, a warp a
+// row at a time.
+constexpr int kCombineRows = 32;
 __global__ void __launch_bounds__(256)
 paged_prompt_combine_kernel(const PagedArgs a, int tiles, int min_rows) {
   grid_dependency_wait();
   grid_launch_dependents();
+  constexpr int kParts = kSlotRows / kCombineRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = blockIdx.x / (kSlotRows / 8);
-  const int rs = (blockIdx.x % (kSlotRows / 8)) * 8 + warp;
+  const int pair = blockIdx.x / kParts;
   const int slot = pair / a.Hkv, hk = pair - slot * a.Hkv;
   int b = 0, row0 = 0;
-  if (slot_steps(a, slot, min_rows, a.q_start, b, row0) < 0) return;
-  const RowRange rr = rows_of(a.q_start, b, a.T);
-  const int r = row0 + rs;
-  if (r >= rr.n * a.g) return;
+  if (slot_steps(a, slot, min_rows, a.q_start, b, row0) <= kMinChunk) return;   // not split
   const int2 mt = a.meta[pair];
   if (mt.y <= 1) return;
-  const float* base = a.parts + (static_cast<size_t>(mt.x) * kSlotRows + rs) * kPartFloats;
-  const size_t step = static_cast<size_t>(kSlotRows) * kPartFloats;
-  float M = -INFINITY;
-  for (int p = lane; p < mt.y; p += 32) M = fmaxf(M, base[p * step]);
+  const RowRange rr = rows_of(a.q_start, b, a.T);
+  for (int i = warp; i < kCombineRows; i += 8) {
+    const int rs = (blockIdx.x - pair * kParts) * kCombineRows + i;
+    const int r = row0 + rs;
+    if (r >= rr.n * a.g) return;
+    const float* base = a.parts + (static_cast<size_t>(mt.x) * kSlotRows + rs) * kPartFloats;
+    const size_t step = static_cast<size_t>(kSlotRows) * kPartFloats;
+    float M = -INFINITY;
+    for (int p = lane; p < mt.y; p += 32) M = fmaxf(M, base[p * step]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float den = 0.0f;
-  float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float den = 0.0f;
+    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-  for (int p = 0; p < mt.y; ++p) {
-    const float* pp = base + p * step;
-    const float m = pp[0];
-    const float f = m == -INFINITY ? 0.0f : fast_exp2(m - M);
-    const float4 v = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
-    den += f * pp[1];
-    num.x += f * v.x;
-    num.y += f * v.y;
-    num.z += f * v.z;
-    num.w += f * v.w;
+    for (int p = 0; p < mt.y; ++p) {
+      const float* pp = base + p * step;
+      const float m = pp[0];
+      const float f = m == -INFINITY ? 0.0f : fast_exp2(m - M);
+      const float4 v = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
+      den += f * pp[1];
+      num.x += f * v.x;
+      num.y += f * v.y;
+      num.z += f * v.z;
+      num.w += f * v.w;
+    }
+    const int qi = r / a.g;
+    store_row4(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g + (r - qi * a.g)) *
+                           kHeadDim + 4 * lane, num, den == 0.0f ? 0.0f : __frcp_rn(den));
   }
-  const int qi = r / a.g;
-  store_row4(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g + (r - qi * a.g)) *
-                         kHeadDim + 4 * lane, num, den == 0.0f ? 0.0f : __frcp_rn(den));
 }
 
 // Once per device: opt in to the shared memory, and check the registers.  The
@@ -787,7 +792,7 @@ int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, cu
                                 kThreads, kSmemBytes, s, a, p.tiles, p.prompt_target, min_rows))
     return st;
   if (!p.prompt_combine) return QOQ_OK;
-  const long long ctas = static_cast<long long>(p.tiles) * a.Hkv * (kSlotRows / 8);
+  const long long ctas = static_cast<long long>(p.tiles) * a.Hkv * (kSlotRows / kCombineRows);
   return launch_dependent(paged_prompt_combine_kernel, dim3(static_cast<unsigned>(ctas)), 256, 0, s,
                           a, p.tiles, min_rows);
 }
