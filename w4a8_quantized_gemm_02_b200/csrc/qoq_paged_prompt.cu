@@ -12,11 +12,12 @@
 // errors of the output's own size.  Centred codes keep what the rounding of W
 // touches as small as v^ about its vector's middle.
 //
-// Warps.  Warpgroups 0 and 1 hold a row a thread of one tile each (softmax);
-// warpgroup 2 turns codes into FP16 tiles; one thread of warpgroup 3 issues the
-// MMAs: for each tile in turn O += W V and then the next S, so one tile's
-// products run while the other's softmax does.  W overwrites S in tensor memory
-// (512 columns: S and O of both tiles).
+// Warps.  Warpgroups 0 and 1 do the softmax of one tile each; warpgroup 2 turns codes
+// into FP16 tiles; one thread of warpgroup 3 issues the MMAs of whichever tile is ready.
+// Tensor memory (512 columns) holds S and O of both tiles; W overwrites the scores it
+// came from.  A step's softmax goes by halves of 64 tokens, so that O += W V of the
+// first half runs beside the second half's softmax, and one tile's products beside the
+// other's softmax.
 //
 // Layouts.  The cache's nibble order is the register layout of warp MMAs, so a
 // lane of the producer holds, for one token, dimensions 16 w + 2 tig + {0, 1, 8,
@@ -55,19 +56,20 @@ constexpr int kSlotRows = 256;
 constexpr int kTile = 128;                      // rows of a tile, tokens of a step
 constexpr int kMinChunk = 8;                    // steps: a split's least length
 constexpr float kRaise = 2.9f;                  // 2^2.9 * 131008 / 15 is an FP16 number
+constexpr float kHeadroom = 2.0f;               // a raised reference lies this far above the
+                                                // score: a raise rescales O, and one is enough
 constexpr int kMaxStagedSeqs = 2048;
 
 // Shared memory: Q 2 tiles x 2 halves of 64 dimensions x [128 rows][128 bytes],
-// K and V twice each, 2 halves x [128][128 bytes] (128-byte swizzle), then the
-// scales of two steps: per column pair (s_K, s_K', m_K, m_K') and (s_V, s_V', m_V, m_V').
+// K and V twice each, 2 halves x [128][128 bytes] (128-byte swizzle).
 constexpr uint32_t kHalf = 16384;
-constexpr uint32_t kQ = 0, kK = 4 * kHalf, kV = kK + 4 * kHalf, kScales = kV + 4 * kHalf;
-constexpr uint32_t kScaleStage = 2 * 64 * 16;
-constexpr uint32_t kSmemBytes = kScales + 2 * kScaleStage + 1024;   // + alignment
+constexpr uint32_t kQ = 0, kK = 4 * kHalf, kV = kK + 4 * kHalf;
+constexpr uint32_t kSmemBytes = kV + 4 * kHalf + 1024;   // + alignment
 
 struct Bars {
-  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], c_full[2], s_full[2], p_full[2],
-      o_full;
+  uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], c_full[2];
+  uint64_t s_full[2], p_full[2][2];        // [tile], [tile][half step]
+  uint64_t o_done[2], o_full;
 };
 
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -88,9 +90,11 @@ __device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, u
       "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// Instruction descriptor: FP16 A and B, K-major, FP32 accumulator, 128 x 128.
-constexpr uint32_t kIdesc = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) |
-                            (static_cast<uint32_t>(kTile >> 4) << 24);
+// Instruction descriptor: FP16 A and B, K-major, FP32 accumulator, 128 x n.
+constexpr uint32_t idesc_f16(int n) {
+  return (1u << 4) | (static_cast<uint32_t>(n >> 3) << 17) |
+         (static_cast<uint32_t>(kTile >> 4) << 24);
+}
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
   uint32_t* u = reinterpret_cast<uint32_t*>(r);
@@ -106,19 +110,62 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* r) {
       : "r"(taddr)
       : "memory");
 }
-// The wait that completes loads, naming their registers so that no use moves
-// above it.
-__device__ __forceinline__ void tmem_ld_done(float* r) {
-  uint32_t* u = reinterpret_cast<uint32_t*>(r);
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(u[0]), "+r"(u[1]), "+r"(u[2]), "+r"(u[3]), "+r"(u[4]), "+r"(u[5]),
-                 "+r"(u[6]), "+r"(u[7]), "+r"(u[8]), "+r"(u[9]), "+r"(u[10]), "+r"(u[11]),
-                 "+r"(u[12]), "+r"(u[13]), "+r"(u[14]), "+r"(u[15]), "+r"(u[16]), "+r"(u[17]),
-                 "+r"(u[18]), "+r"(u[19]), "+r"(u[20]), "+r"(u[21]), "+r"(u[22]), "+r"(u[23]),
-                 "+r"(u[24]), "+r"(u[25]), "+r"(u[26]), "+r"(u[27])
-               :
-               : "memory");
-  asm volatile("" : "+r"(u[28]), "+r"(u[29]), "+r"(u[30]), "+r"(u[31])::"memory");
+// Tensor memory by 16 lanes: thread (g, t) = (lane / 4, lane mod 4) of the warp gets, of
+// every 8 columns, columns 2 t and 2 t + 1 of rows g (registers 4 k, 4 k + 1) and g + 8
+// (4 k + 2, 4 k + 3).
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, float (&r)[32]) {
+  uint32_t (&u)[32] = reinterpret_cast<uint32_t (&)[32]>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31"
+      "}, [%32];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7]),
+        "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]), "=r"(u[14]), "=r"(u[15]),
+        "=r"(u[16]), "=r"(u[17]), "=r"(u[18]), "=r"(u[19]), "=r"(u[20]), "=r"(u[21]), "=r"(u[22]), "=r"(u[23]),
+        "=r"(u[24]), "=r"(u[25]), "=r"(u[26]), "=r"(u[27]), "=r"(u[28]), "=r"(u[29]), "=r"(u[30]), "=r"(u[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_16x32(uint32_t taddr, float (&r)[16]) {
+  uint32_t (&u)[16] = reinterpret_cast<uint32_t (&)[16]>(r);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {"
+      "%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15"
+      "}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_16x32(uint32_t taddr, const float (&r)[16]) {
+  const uint32_t (&u)[16] = reinterpret_cast<const uint32_t (&)[16]>(r);
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+      "};" ::"r"(taddr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+      "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
+// 32 columns of 32 bits: of every 4 columns, column t of rows g (register 2 k) and
+// g + 8 (2 k + 1).
+__device__ __forceinline__ void tmem_st_16x32h(uint32_t taddr, const uint32_t (&u)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {"
+      "%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16"
+      "};" ::"r"(taddr),
+      "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]),
+      "r"(u[8]), "r"(u[9]), "r"(u[10]), "r"(u[11]), "r"(u[12]), "r"(u[13]), "r"(u[14]), "r"(u[15])
+      : "memory");
+}
+// After the wait that completes loads: names a load's registers, so that no use of them
+// moves above it.
+template <int N>
+__device__ __forceinline__ void keep(float (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
 }
 
 // Two FP32 operations an instruction.
@@ -162,11 +209,8 @@ __device__ __forceinline__ void regs_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-// Token (within its 32) at column position q of S, and back.
-__host__ __device__ constexpr int token_at(int q) {
-  return 16 * ((q >> 2) & 1) + 2 * (q >> 3) + (q & 1) + 8 * ((q >> 1) & 1);
-}
-__device__ __forceinline__ int column_of(int tok) {    // tok: 0 .. 31
+// Column position of token 0 .. 31 (of its 32) in S.
+__device__ __forceinline__ int column_of(int tok) {
   return 8 * ((tok & 7) >> 1) + 4 * (tok >> 4) + 2 * ((tok >> 3) & 1) + (tok & 1);
 }
 
@@ -181,11 +225,12 @@ __device__ __forceinline__ void sts16(uint32_t at, uint4 v) {
                "r"(v.w)
                : "memory");
 }
-__device__ __forceinline__ float4 lds16(uint32_t at) {
-  float4 v;
-  asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-               : "r"(at));
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(at)
+               : "memory");
   return v;
 }
 
@@ -195,6 +240,37 @@ __device__ __forceinline__ uint32_t centred(uint32_t word, int s) {
   const uint32_t n = and_or(word >> s, 0x000f000fu, 0x64006400u);
   const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&n), __float2half2_rn(1032.0f));
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// mbar_wait by tests that never suspend the thread: what these waits hand over is on the
+// path from one product to the next, and waking up from a suspension takes longer than
+// the product.  Bounded the same way.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity,
+                                          volatile uint32_t* abort_flag, uint32_t err) {
+  if (mbar_test(bar, parity)) return true;
+  const long long t0 = sm_clock();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 256; ++i)
+      if (mbar_test(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (sm_clock() - t0 > kWaitLimitCycles) {
+      *abort_flag = 1u;
+      atomicOr(&g_prompt_error, err);
+      return false;
+    }
+  }
 }
 
 struct Unit {
@@ -329,6 +405,9 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_abort;
   __shared__ uint32_t s_absent[2][4];       // per step: bit per 16-token block and producer warp
+  // scales of two steps, per column pair: (s_K, s_K', m_K, m_K') and (s_V, s_V', m_V, m_V')
+  __shared__ float4 s_scale[2][2][kTile / 2];
+  __shared__ float s_row[3][kSlotRows];     // Q sums; then l, offset sum and reference
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
   const uint32_t s0 = smem_u32(smem);
@@ -346,15 +425,16 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
 
   if (tid == 0) {
     s_abort = 0u;
-    mbar_init(bar(bars.q_full), 256);
+    mbar_init(bar(bars.q_full), 8);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(bar(bars.k_full[i]), 128);
-      mbar_init(bar(bars.v_full[i]), 128);
-      mbar_init(bar(bars.c_full[i]), 128);
+      mbar_init(bar(bars.k_full[i]), 4);
+      mbar_init(bar(bars.v_full[i]), 4);
+      mbar_init(bar(bars.c_full[i]), 4);
       mbar_init(bar(bars.k_empty[i]), 1);
       mbar_init(bar(bars.v_empty[i]), 1);
+      mbar_init(bar(bars.o_done[i]), 1);
       mbar_init(bar(bars.s_full[i]), 1);
-      mbar_init(bar(bars.p_full[i]), 128);
+      for (int h = 0; h < 2; ++h) mbar_init(bar(bars.p_full[i][h]), 4);
     }
     mbar_init(bar(bars.o_full), 1);
     fence_mbar_init();
@@ -367,191 +447,281 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
   tc_fence_after_sync();
   const uint32_t tmem = s_tmem;
   auto wait = [&](uint64_t& x, uint32_t parity, uint32_t err) {
-    return mbar_wait(smem_u32(&x), parity, &s_abort, &g_prompt_error, err);
+    return __all_sync(0xffffffffu, mbar_wait(smem_u32(&x), parity, &s_abort, &g_prompt_error,
+                                             err)) != 0;
+  };
+  // (one arrival a warp: 128 in a row take longer than what they announce)
+  auto arrive = [&](uint64_t& x) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&x));
   };
 
   if (warp < 8) {
     // ---------------------------------------------------------------- softmax
-    regs_inc<192>();
-    const int x = warp >> 2, row = 32 * (warp & 3) + lane;       // tile and row of it
-    const int r = u.row0 + kTile * x + row;
-    const int qi = r / g;
-    const bool mine = r < R;
-    const __half* q = a.Q + static_cast<size_t>(rr.first + (mine ? qi : 0)) * a.ldq +
-                      static_cast<size_t>(u.hk * g + (mine ? r - qi * g : 0)) * kHeadDim;
-    float qsum = 0.0f;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      // 32 dimensions, words w = 2k and 2k + 1: four bytes (dimensions d, d + 1) at
-      // 16 w + 2 tig and 16 w + 8 + 2 tig go to chunk 4 tig + k
-      uint32_t d[2][8];
+    regs_inc<168>();
+    const int x = warp >> 2;         // tile
+    // Q, four lanes a row and 8 rows a turn: lane part k has 32 dimensions, words w = 2k
+    // and 2k + 1, whose four bytes (dimensions d, d + 1) at 16 w + 2 tig and
+    // 16 w + 8 + 2 tig go to chunk 4 tig + k
+    {
+      const int k = lane & 3;
+      uint4 v[4][4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint4 v = mine ? *reinterpret_cast<const uint4*>(q + 32 * k + 8 * i)
-                             : make_uint4(0u, 0u, 0u, 0u);
-        d[i >> 1][4 * (i & 1) + 0] = v.x;
-        d[i >> 1][4 * (i & 1) + 1] = v.y;
-        d[i >> 1][4 * (i & 1) + 2] = v.z;
-        d[i >> 1][4 * (i & 1) + 3] = v.w;
+        const int r = u.row0 + kTile * x + 32 * (warp & 3) + 8 * i + (lane >> 2), qi = r / g;
+        const uint4* q = reinterpret_cast<const uint4*>(
+            a.Q + static_cast<size_t>(rr.first + (r < R ? qi : 0)) * a.ldq +
+            static_cast<size_t>(u.hk * g + (r < R ? r - qi * g : 0)) * kHeadDim + 32 * k);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[i][c] = r < R ? q[c] : make_uint4(0u, 0u, 0u, 0u);
       }
 #pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&d[i >> 3][i & 7]));
-        qsum += f.x + f.y;
-      }
+      for (int i = 0; i < 4; ++i) {
+        const int row = 32 * (warp & 3) + 8 * i + (lane >> 2);
+        const uint32_t d[16] = {v[i][0].x, v[i][0].y, v[i][0].z, v[i][0].w, v[i][1].x, v[i][1].y,
+                                v[i][1].z, v[i][1].w, v[i][2].x, v[i][2].y, v[i][2].z, v[i][2].w,
+                                v[i][3].x, v[i][3].y, v[i][3].z, v[i][3].w};
+        float qsum = 0.0f;
 #pragma unroll
-      for (int tig = 0; tig < 4; ++tig)
-        sts16(s0 + kQ + x * 2 * kHalf + tile_at(row, 4 * tig + k),
-              make_uint4(d[0][tig], d[0][4 + tig], d[1][tig], d[1][4 + tig]));
+        for (int c = 0; c < 16; ++c) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&d[c]));
+          qsum += f.x + f.y;
+        }
+        qsum += __shfl_xor_sync(0xffffffffu, qsum, 1);
+        qsum += __shfl_xor_sync(0xffffffffu, qsum, 2);
+#pragma unroll
+        for (int tig = 0; tig < 4; ++tig)
+          sts16(s0 + kQ + x * 2 * kHalf + tile_at(row, 4 * tig + k),
+                make_uint4(d[tig], d[4 + tig], d[8 + tig], d[12 + tig]));
+        if (k == 0) s_row[0][kTile * x + row] = qsum;
+      }
     }
     fence_proxy_async_smem();
-    mbar_arrive(bar(bars.q_full));
+    arrive(bars.q_full);
 
-    const int lim = mine ? visible(position_of(seqlen, rr.n, qi), len) : 0;
-    float mref = 0.0f, l = 0.0f, off = 0.0f;
-    const F2 q2 = pair2(qsum, qsum);
+    // Scores are read 16 lanes at a time: thread (gr, t) has columns 2 t and 2 t + 1 of
+    // every 8, of rows gr, gr + 8, gr + 16 and gr + 24 of its warp's 32.  A column's
+    // scales then serve four rows: with a row a thread they came to 4096 cycles of
+    // shared-memory reads a step, twice the products' time.
+    const int gr = lane >> 2, t = lane & 3;
+    int lim[4];
+    F2 q2[4], ref2[4], l2[4], off2[4];
+    bool seen[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int ri = 32 * (warp & 3) + 8 * i + gr, rg = u.row0 + kTile * x + ri;
+      lim[i] = rg < R ? visible(position_of(seqlen, rr.n, rg / g), len) : 0;
+      const float qs = s_row[0][kTile * x + ri];
+      q2[i] = pair2(qs, qs);
+      ref2[i] = l2[i] = off2[i] = pair2(0.0f, 0.0f);     // ref: minus the reference
+      seen[i] = false;
+    }
+    // the tokens that every row of the warp sees
+    const int least = __reduce_min_sync(0xffffffffu, min(min(lim[0], lim[1]), min(lim[2], lim[3])));
+    // token of column 8 k + 2 t + e in its step: first_token + 32 (k / 4) + 2 (k mod 4) + e
+    const int first_token = 16 * (t >> 1) + 8 * (t & 1);
     const uint32_t t_s = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kTile * x;
-    const uint32_t t_o = t_s + 2 * kTile;
+    const uint32_t t_o = t_s + 2 * kTile, half16 = 16u << 16;
     bool ok = true;
     if (x == 0 || two) {
-      for (int j = 0; j < steps; ++j) {
-        ok = wait(bars.s_full[x], j & 1, kErrEpilogue) &&
-             wait(bars.c_full[j & 1], (j >> 1) & 1, kErrEpilogue);
-        if (!__all_sync(0xffffffffu, ok)) {
-          ok = false;
-          break;
+      uint32_t absent2 = 0;
+      for (int hs = 0; hs < 2 * steps; ++hs) {
+        const int j = hs >> 1, hf = hs & 1;
+        if (hf == 0) {
+          ok = wait(bars.s_full[x], j & 1, kErrEpilogue) &&
+               wait(bars.c_full[j & 1], (j >> 1) & 1, kErrEpilogue);
+          if (!ok) break;
+          tc_fence_after_sync();
+          absent2 = s_absent[j & 1][0] | s_absent[j & 1][1] | s_absent[j & 1][2] | s_absent[j & 1][3];
         }
-        tc_fence_after_sync();
-        float s[kTile];
+        const uint32_t t_h = t_s + (kTile / 2) * hf;
+        F2 s[4][8];          // row i, columns 8 k + 2 t and + 1
+        {
+          float r[2][32];    // rows gr and gr + 8, then gr + 16 and gr + 24
+          tmem_ld_16x64(t_h, r[0]);
+          tmem_ld_16x64(t_h + half16, r[1]);
+          tmem_ld_wait();
+          keep(r[0]);
+          keep(r[1]);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, s + 32 * c);
+          for (int i = 0; i < 4; ++i)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_done(s + 32 * c);
-        const uint32_t sc = s0 + kScales + (j & 1) * kScaleStage;
-        // x - mref
-        const F2 ref = pair2(-mref, -mref);
-#pragma unroll
-        for (int c = 0; c < kTile; c += 2) {
-          const float4 kc = lds16(sc + 8 * c);
-          const F2 v = fma2(pair2(s[c], s[c + 1]), pair2(kc.x, kc.y),
-                            fma2(q2, pair2(kc.z, kc.w), ref));
-          s[c] = v.f[0];
-          s[c + 1] = v.f[1];
+            for (int k = 0; k < 8; ++k)
+              s[i][k] = pair2(r[i >> 1][4 * k + 2 * (i & 1)], r[i >> 1][4 * k + 2 * (i & 1) + 1]);
         }
-        // tokens that the row does not see, or in no page
-        const int rel = lim - (u.step0 + j) * kTile;
-        const uint32_t absent = s_absent[j & 1][0] | s_absent[j & 1][1] | s_absent[j & 1][2] |
-                                s_absent[j & 1][3];
-        if (__any_sync(0xffffffffu, rel < kTile || absent != 0u)) {
+        const float4* sk = s_scale[j & 1][0] + 32 * hf + t;
+        const float4* sv = s_scale[j & 1][1] + 32 * hf + t;
+        // scores less the reference
 #pragma unroll
-          for (int c = 0; c < kTile; ++c) {
-            const int tok = 32 * (c >> 5) + token_at(c & 31);
-            if (tok >= rel || ((absent >> (tok >> 4)) & 1u)) s[c] = -INFINITY;
+        for (int k = 0; k < 8; ++k) {
+          const float4 kc = sk[4 * k];
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            s[i][k] = fma2(s[i][k], pair2(kc.x, kc.y), fma2(q2[i], pair2(kc.z, kc.w), ref2[i]));
+        }
+        // tokens that a row does not see, or in no page
+        const int seen_here = (u.step0 + j) * kTile + (kTile / 2) * hf;
+        const uint32_t absent = (absent2 >> (4 * hf)) & 15u;
+        if (least - seen_here < kTile / 2 || absent != 0u) {        // (the same for the warp)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rel = lim[i] - seen_here - first_token;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const bool gone = (absent >> (2 * (k >> 2) + (t >> 1))) & 1u;
+              if (32 * (k >> 2) + 2 * (k & 3) >= rel || gone) s[i][k].f[0] = -INFINITY;
+              if (32 * (k >> 2) + 2 * (k & 3) + 1 >= rel || gone) s[i][k].f[1] = -INFINITY;
+            }
           }
         }
-        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        float high[4];
+        bool raise = false, up_row[4];
 #pragma unroll
-        for (int c = 0; c < kTile; c += 2) top[(c >> 1) & 3] = max3(top[(c >> 1) & 3], s[c], s[c + 1]);
-        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        // raise the reference: past the threshold, or at the first token seen
-        const bool raise = high > kRaise || (l == 0.0f && high > -INFINITY);
+        for (int i = 0; i < 4; ++i) {
+          float a0 = -INFINITY, a1 = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 8; k += 2) {
+            a0 = max3(a0, s[i][k].f[0], s[i][k].f[1]);
+            a1 = max3(a1, s[i][k + 1].f[0], s[i][k + 1].f[1]);
+          }
+          high[i] = fmaxf(a0, a1);
+          high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 1));
+          high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 2));
+          // raise the reference: past the threshold, or at the first token seen
+          up_row[i] = high[i] > kRaise || (!seen[i] && high[i] > -INFINITY);
+          raise |= up_row[i];
+        }
         if (__any_sync(0xffffffffu, raise)) {
-          const float up = raise ? high : 0.0f;
-          mref += up;
-          const float al = l == 0.0f ? 1.0f : fast_exp2(-up);
-          l *= al;
-          off *= al;
-          const F2 d2 = pair2(-up, -up), al2 = pair2(al, al);
+          float al[4];
 #pragma unroll
-          for (int c = 0; c < kTile; c += 2) {
-            const F2 v = add2(pair2(s[c], s[c + 1]), d2);
-            s[c] = v.f[0];
-            s[c + 1] = v.f[1];
+          for (int i = 0; i < 4; ++i) {
+            const float up = up_row[i] ? high[i] + kHeadroom : 0.0f;
+            al[i] = seen[i] ? fast_exp2(-up) : 1.0f;
+            seen[i] |= up_row[i];
+            const F2 d2 = pair2(-up, -up), al2 = pair2(al[i], al[i]);
+            ref2[i] = add2(ref2[i], d2);
+            l2[i] = mul2(l2[i], al2);
+            off2[i] = mul2(off2[i], al2);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[i][k] = add2(s[i][k], d2);
           }
-          if (j > 0) {
-            // (the products that wrote O are complete: this step's S came after
-            // them)
-#pragma unroll 1
-            for (int c = 0; c < kTile; c += 32) {
-              float o[32];
-              tmem_ld32(t_o + c, o);
-              tmem_ld_done(o);
+          if (hs > 0) {
+            // the last product into O (for a first half the scores came after it)
+            ok = wait(bars.o_done[x], (hs - 1) & 1, kErrEpilogue);
+            if (!ok) break;
+            tc_fence_after_sync();
 #pragma unroll
-              for (int k = 0; k < 32; k += 2) {
-                const F2 v = mul2(pair2(o[k], o[k + 1]), al2);
-                o[k] = v.f[0];
-                o[k + 1] = v.f[1];
+            for (int h = 0; h < 2; ++h) {
+#pragma unroll 1
+              for (int c = 0; c < kTile; c += 32) {
+                float o[16];
+                tmem_ld_16x32(t_o + h * half16 + c, o);
+                tmem_ld_wait();
+                keep(o);
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] *= al[2 * h + ((k >> 1) & 1)];
+                tmem_st_16x32(t_o + h * half16 + c, o);
               }
-              tmem_st_32x32b_x32(t_o + c, *reinterpret_cast<const uint32_t(*)[32]>(o));
             }
           }
         }
         // weights
-        F2 l2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
-        F2 o2[2] = {pair2(0.0f, 0.0f), pair2(0.0f, 0.0f)};
+        uint32_t w[2][16];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t w[32];
+        for (int k = 0; k < 8; ++k) {
+          const float4 vc = sv[4 * k];
 #pragma unroll
-          for (int k = 0; k < 32; ++k) {
-            const int c = 64 * h + 2 * k;
-            const float4 vc = lds16(sc + 1024 + 8 * c);
-            const F2 p = pair2(fast_exp2(s[c]), fast_exp2(s[c + 1]));
-            l2[k & 1] = add2(l2[k & 1], p);
-            o2[k & 1] = fma2(p, pair2(vc.z, vc.w), o2[k & 1]);
-            const F2 v = mul2(p, pair2(vc.x, vc.y));
-            w[k] = pack_h2(v.f[0], v.f[1]);
+          for (int i = 0; i < 4; ++i) {
+            const F2 p = pair2(fast_exp2(s[i][k].f[0]), fast_exp2(s[i][k].f[1]));
+            l2[i] = add2(l2[i], p);
+            off2[i] = fma2(p, pair2(vc.z, vc.w), off2[i]);
+            const F2 d = mul2(p, pair2(vc.x, vc.y));
+            w[i >> 1][2 * k + (i & 1)] = pack_h2(d.f[0], d.f[1]);
           }
-          tmem_st_32x32b_x32(t_s + 32 * h, w);
         }
-        l2[0] = add2(l2[0], l2[1]);
-        o2[0] = add2(o2[0], o2[1]);
-        l += l2[0].f[0] + l2[0].f[1];
-        off += o2[0].f[0] + o2[0].f[1];
+        tmem_st_16x32h(t_h, w[0]);
+        tmem_st_16x32h(t_h + half16, w[1]);
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(bar(bars.p_full[x]));
+        arrive(bars.p_full[x][hf]);
       }
+      // the rows' sums, for the epilogue's row a thread
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float li = l2[i].f[0] + l2[i].f[1], oi = off2[i].f[0] + off2[i].f[1];
+#pragma unroll
+        for (int d = 1; d < 4; d <<= 1) {
+          li += __shfl_xor_sync(0xffffffffu, li, d);
+          oi += __shfl_xor_sync(0xffffffffu, oi, d);
+        }
+        if (t == 0) {
+          const int ri = kTile * x + 32 * (warp & 3) + 8 * i + gr;
+          s_row[0][ri] = li;
+          s_row[1][ri] = oi;
+          s_row[2][ri] = -ref2[i].f[0];
+        }
+      }
+      __syncwarp();        // (a warp reads the rows it wrote)
+      const float l = s_row[0][tid], off = s_row[1][tid], mref = s_row[2][tid];
       if (steps > 0 && ok) ok = wait(bars.o_full, 0, kErrEpilogue);
-      ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         tc_fence_after_sync();
         const bool whole = u.nsplit == 1;
         // (a row that saw no token has l = 0; its O is zero or was not written)
         const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
-        float* part = nullptr;
-        __half* dst = nullptr;
-        if (whole)
-          dst = a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + u.hk * g + (r - qi * g)) *
-                            kHeadDim;
-        else
-          part = a.parts + (static_cast<size_t>(u.part) * kSlotRows + kTile * x + row) *
-                               kPartFloats;
-        if (!whole && mine) {
-          part[0] = l == 0.0f ? -INFINITY : mref;
-          part[1] = l;
-        }
+        const int rows0 = u.row0 + kTile * x + 32 * (warp & 3);      // the warp's first row
+        const int left = R - rows0 < 32 ? R - rows0 : 32;
+        // A row a thread comes out of tensor memory; rows leave by way of the warp's 16 KB
+        // of shared memory (the products are done with it), 16 bytes a lane along a row.
+        // Chunk c of row r lies at c ^ (r & 7).
+        const uint32_t mine = s0 + warp * 16384 + lane * 512;
 #pragma unroll 1
         for (int c = 0; c < kTile; c += 32) {
           float o[32];
           if (steps > 0) {
             tmem_ld32(t_o + c, o);
-            tmem_ld_done(o);
+            tmem_ld_wait();
+            keep(o);
           }
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
             float v[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] = l == 0.0f ? 0.0f : o[k + i] + off;
-            if (mine) {
-              if (whole) {
-                store_row8(dst + c + k, v, inv);
-              } else {
-                *reinterpret_cast<float4*>(part + 4 + c + k) = make_float4(v[0], v[1], v[2], v[3]);
-                *reinterpret_cast<float4*>(part + 8 + c + k) = make_float4(v[4], v[5], v[6], v[7]);
-              }
+            if (whole) {
+              sts16(mine + ((((c + k) >> 3) ^ (lane & 7)) << 4),
+                    make_uint4(pack_h2(v[0] * inv, v[1] * inv), pack_h2(v[2] * inv, v[3] * inv),
+                               pack_h2(v[4] * inv, v[5] * inv), pack_h2(v[6] * inv, v[7] * inv)));
+            } else {
+#pragma unroll
+              for (int i = 0; i < 2; ++i)
+                sts16(mine + (((((c + k) >> 2) + i) ^ (lane & 7)) << 4),
+                      make_uint4(__float_as_uint(v[4 * i]), __float_as_uint(v[4 * i + 1]),
+                                 __float_as_uint(v[4 * i + 2]), __float_as_uint(v[4 * i + 3])));
             }
           }
+        }
+        __syncwarp();
+        const uint32_t from = s0 + warp * 16384;
+        if (whole) {
+#pragma unroll 4
+          for (int i = lane >> 4; i < left; i += 2) {
+            const int qi = (rows0 + i) / g, c = lane & 15;
+            __half* dst = a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + u.hk * g +
+                                   (rows0 + i - qi * g)) * kHeadDim + 8 * c;
+            *reinterpret_cast<uint4*>(dst) = lds16(from + i * 512 + ((c ^ (i & 7)) << 4));
+          }
+        } else {
+          float* part = a.parts + (static_cast<size_t>(u.part) * kSlotRows + kTile * x +
+                                   32 * (warp & 3)) * kPartFloats;
+          if (lane < left) {
+            part[lane * kPartFloats] = l == 0.0f ? -INFINITY : mref;
+            part[lane * kPartFloats + 1] = l;
+          }
+#pragma unroll 4
+          for (int i = 0; i < left; ++i)
+            *reinterpret_cast<uint4*>(part + i * kPartFloats + 4 + 4 * lane) =
+                lds16(from + i * 512 + ((lane ^ (i & 7)) << 4));
         }
       }
     }
@@ -618,7 +788,7 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
         }
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(bars.k_full[st]));
+      arrive(bars.k_full[st]);
 
       if (use > 0 && !wait(bars.v_empty[st], (use - 1) & 1, kErrProducer)) break;
       {
@@ -628,17 +798,15 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
         // (a slot past the length may hold anything: its scales count as zero)
         const bool in = tok < len;
         const int c = 32 * pw + column_of(lane);
-        const uint32_t at = s0 + kScales + st * kScaleStage + 16 * (c >> 1) + 4 * (c & 1);
-        auto put = [&](uint32_t d, float v) {
-          asm volatile("st.shared.f32 [%0], %1;" ::"r"(at + d), "f"(in ? v : 0.0f) : "memory");
-        };
-        put(0, fk.x * scale2);
-        put(8, fmaf(8.0f, fk.x, fk.y) * scale2);
-        put(1024, fv.x);
-        put(1024 + 8, fmaf(8.0f, fv.x, fv.y));
+        float* ks = reinterpret_cast<float*>(&s_scale[st][0][c >> 1]) + (c & 1);
+        float* vs = reinterpret_cast<float*>(&s_scale[st][1][c >> 1]) + (c & 1);
+        ks[0] = in ? fk.x * scale2 : 0.0f;
+        ks[2] = in ? fmaf(8.0f, fk.x, fk.y) * scale2 : 0.0f;
+        vs[0] = in ? fv.x : 0.0f;
+        vs[2] = in ? fmaf(8.0f, fv.x, fv.y) : 0.0f;
         if (lane == 0) s_absent[st][pw] = gone;
       }
-      mbar_arrive(bar(bars.c_full[st]));
+      arrive(bars.c_full[st]);
       // V tile: row dimension, chunk of tokens 32 pw + 8 tig ..
       const uint32_t vt = s0 + kV + st * 2 * kHalf;
 #pragma unroll
@@ -653,52 +821,85 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
                            centred(wb, 4 * j0 + 8)));
       }
       fence_proxy_async_smem();
-      mbar_arrive(bar(bars.v_full[st]));
+      arrive(bars.v_full[st]);
       if (j + 1 < steps) fetch(u.step0 + j + 1);
     }
   } else {
-    regs_dec<32>();
+    regs_dec<80>();
     if (warp == 12 && lane == 0 && steps > 0) {
       // ------------------------------------------------------------------ MMA
       const uint32_t tiles_here = two ? 2 : 1;
+      auto spin = [&](uint64_t& x, uint32_t parity, uint32_t err) {
+        return spin_wait(smem_u32(&x), parity, &s_abort, err);
+      };
+      // (descriptors differ in their low word only: an address in units of 16 bytes)
+      const uint64_t dq = smem_desc_sw128(s0 + kQ), dk = smem_desc_sw128(s0 + kK);
+      const uint64_t dv = smem_desc_sw128(s0 + kV);
       auto scores = [&](uint32_t x, int st) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
-          const uint32_t at = (ks >> 2) * kHalf + (ks & 3) * 32;
-          mma_f16_ss(tmem + kTile * x, smem_desc_sw128(s0 + kQ + x * 2 * kHalf + at),
-                     smem_desc_sw128(s0 + kK + st * 2 * kHalf + at), kIdesc, ks > 0);
+          const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+          mma_f16_ss(tmem + kTile * x, dq + ((x * 2 * kHalf) >> 4) + at,
+                     dk + ((st * 2 * kHalf) >> 4) + at, idesc_f16(kTile), ks > 0);
         }
         mma_commit(bar(bars.s_full[x]));
       };
-      bool ok = wait(bars.q_full, 0, kErrMma) && wait(bars.k_full[0], 0, kErrMma);
+      bool ok = spin(bars.q_full, 0, kErrMma) && spin(bars.k_full[0], 0, kErrMma);
       if (ok) {
         tc_fence_after_sync();
         for (uint32_t x = 0; x < tiles_here; ++x) scores(x, 0);
         mma_commit(bar(bars.k_empty[0]));
       }
-      for (int j = 0; j < steps && ok; ++j) {
-        const int st = j & 1, next = (j + 1) & 1;
-        for (uint32_t x = 0; x < tiles_here && ok; ++x) {
-          ok = wait(bars.p_full[x], j & 1, kErrMma);
-          if (ok && x == 0) ok = wait(bars.v_full[st], (j >> 1) & 1, kErrMma);
-          if (!ok) break;
+      // per tile the next half step; a stage is free when both tiles have passed it
+      int at[2] = {0, two ? 0 : 2 * steps};
+      int k_ready = 0, v_ready = -1;          // steps whose K and V have arrived
+      long long since = sm_clock();
+      for (int polls = 0; ok && (at[0] < 2 * steps || at[1] < 2 * steps); ++polls) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int hs = at[x], j = hs >> 1, hf = hs & 1, st = j & 1, next = (j + 1) & 1;
+          if (hs >= 2 * steps || !mbar_test(bar(bars.p_full[x][hf]), j & 1)) continue;
+          if (v_ready < j) {
+            ok = spin(bars.v_full[st], (j >> 1) & 1, kErrMma);
+            if (!ok) break;
+            v_ready = j;
+          }
           tc_fence_after_sync();
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_f16_ts(tmem + 2 * kTile + kTile * x, tmem + kTile * x + 8 * ks,
-                       smem_desc_sw128(s0 + kV + st * 2 * kHalf + (ks >> 2) * kHalf + (ks & 3) * 32),
-                       kIdesc, j > 0 || ks > 0);
-          if (j + 1 < steps) {
-            if (x == 0) ok = wait(bars.k_full[next], ((j + 1) >> 1) & 1, kErrMma);
-            if (!ok) break;
-            tc_fence_after_sync();
-            scores(x, next);
+          for (int ks = 0; ks < 4; ++ks)
+            mma_f16_ts(tmem + 2 * kTile + kTile * x, tmem + kTile * x + (kTile / 2) * hf + 8 * ks,
+                       dv + ((st * 2 * kHalf + hf * kHalf + ks * 32) >> 4), idesc_f16(kTile),
+                       hs > 0 || ks > 0);
+          mma_commit(bar(bars.o_done[x]));
+          at[x] = hs + 1;
+          if (hf == 1) {
+            const bool both = at[1 - x] > hs;      // the other tile is done with the step
+            if (both) mma_commit(bar(bars.v_empty[st]));
+            if (j + 1 < steps) {
+              if (k_ready < j + 1) {
+                ok = spin(bars.k_full[next], ((j + 1) >> 1) & 1, kErrMma);
+                if (!ok) break;
+                tc_fence_after_sync();
+                k_ready = j + 1;
+              }
+              scores(x, next);
+              if (both) mma_commit(bar(bars.k_empty[next]));
+            } else if (both) {
+              mma_commit(bar(bars.o_full));
+            }
+          }
+          since = sm_clock();
+          polls = 0;
+        }
+        if (polls > 256) {
+          polls = 0;
+          if (s_abort) ok = false;
+          if (sm_clock() - since > kWaitLimitCycles) {
+            s_abort = 1u;
+            atomicOr(&g_prompt_error, kErrMma);
+            ok = false;
           }
         }
-        if (!ok) break;
-        mma_commit(bar(bars.v_empty[st]));
-        if (j + 1 < steps) mma_commit(bar(bars.k_empty[next]));
-        else mma_commit(bar(bars.o_full));
       }
     }
     __syncwarp();
@@ -756,7 +957,7 @@ paged_prompt_combine_kernel(const PagedArgs a, int tiles, int min_rows) {
 }
 
 // Once per device: opt in to the shared memory, and check the registers.  The
-// kernel's warpgroups split 4 x 128 a thread among them (192, 192, 96, 32); a
+// kernel's warpgroups split 4 x 128 a thread among them (168, 168, 96, 80); a
 // launch with fewer would wait for registers that never come free.
 int prepare_prompt_kernel() {
   static std::atomic<unsigned long long> ready{0};
