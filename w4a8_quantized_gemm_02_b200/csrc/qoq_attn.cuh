@@ -38,7 +38,7 @@ struct PagedPlan {
   int tiles;                // prompt: row slots of the batch
   int prompt_target, prompt_grid;
   bool prompt_combine;
-  size_t meta_off, parts_off, prompt_meta_off, prompt_parts_off, bytes;
+  size_t meta_off, parts_off, prompt_units_off, prompt_meta_off, prompt_parts_off, bytes;
   size_t take(size_t n) {   // the workspace's next n bytes
     const size_t off = bytes;
     bytes += (n + 255) / 256 * 256;
@@ -48,7 +48,9 @@ struct PagedPlan {
 PagedPlan paged_plan(int T, int B, int Hq, int Hkv, int width, int page, int max_q);
 void plan_prompt(PagedPlan& p, int T, int B, int Hq, int Hkv, int width, int page);
 
-int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, cudaStream_t s);
+// `units`: the workspace's list of units.
+int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, void* units,
+                        cudaStream_t s);
 
 // 4 or 8 outputs times `f`, rounded to FP16.
 __device__ __forceinline__ void store_row4(__half* dst, float4 v, float f) {

@@ -699,7 +699,7 @@ extern "C" int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq,
   if (p.prompt) {
     a.meta = p.prompt_combine ? reinterpret_cast<int2*>(w + p.prompt_meta_off) : nullptr;
     a.parts = p.prompt_combine ? reinterpret_cast<float*>(w + p.prompt_parts_off) : nullptr;
-    return launch_paged_prompt(a, p, 4 * p.nt + 1, s);
+    return launch_paged_prompt(a, p, 4 * p.nt + 1, w + p.prompt_units_off, s);
   }
   return QOQ_OK;
 }

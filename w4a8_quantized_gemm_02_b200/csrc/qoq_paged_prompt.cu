@@ -27,9 +27,9 @@
 // are the k index of W V, are token position 8 tig + 4 block + 2 j1 + e of each 32
 // (the rows of the K tile are stored at them).  Every store is 16 bytes.
 //
-// Splits.  All CTAs agree on the tokens a unit walks, from the lengths: long
-// sequences with few rows are split so that no CTA is left with a long one, and
-// a second kernel merges.
+// Splits.  A kernel of one CTA ahead of it looks the lengths over and lists the units
+// of work: long sequences with few rows are split so that no CTA is left with a long
+// one, and a last kernel merges.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -59,6 +59,7 @@ constexpr float kRaise = 2.9f;                  // 2^2.9 * 131008 / 15 is an FP1
 constexpr float kHeadroom = 2.0f;               // a raised reference lies this far above the
                                                 // score: a raise rescales O, and one is enough
 constexpr int kMaxStagedSeqs = 2048;
+constexpr int kSorted = 256;                    // slots up to which units go by length
 
 // Shared memory: Q 2 tiles x 2 halves of 64 dimensions x [128 rows][128 bytes],
 // K and V twice each, 2 halves x [128][128 bytes] (128-byte swizzle).
@@ -273,13 +274,14 @@ __device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity,
   }
 }
 
-struct Unit {
-  int b;             // sequence, -1: nothing to do
-  int part;          // number of this unit among those of split slots
-  int row0;          // first row r of the slot in its sequence
-  int hk, split, nsplit;
-  int slot;
-  int step0, step1;  // steps of 128 tokens
+// A unit of work: steps step0 .. step1 - 1 (of 128 tokens) for the slot of rows from
+// row0 on of sequence b (-1: nothing) and KV head hk.
+struct __align__(16) PromptUnit {
+  int b, row0, hk;
+  int whole;         // the slot is not split
+  int step0, step1;
+  int part;          // its number among the units of split slots
+  int unused;
 };
 
 // Steps of slot `slot` (128-token steps that its last row sees), -1 for a slot
@@ -304,21 +306,26 @@ __device__ __forceinline__ int slot_steps(const PagedArgs& a, int slot, int min_
   return (visible(position_of(a.seqlen[lo], rr.n, last / a.g), len) + kTile - 1) / kTile;
 }
 
-// The unit of this CTA: splits of equal length over the whole batch, the last
-// slots (which see most) first.
-__device__ __forceinline__ Unit find_unit(const PagedArgs& a, int tiles, int target, int min_rows,
-                                          uint8_t* scratch) {
+// The list of units, one CTA.  Splits are equally long over the whole batch: the
+// batch's steps over `target`, kMinChunk at least.  Units go by length where the slots
+// are few (the CTAs that come last should be the shortest), else the last slots, which
+// see most, come first.  meta: per (slot, KV head) its first part and their number, 0
+// for a slot without work and 1 for a whole one.
+__global__ void __launch_bounds__(kThreads)
+paged_prompt_plan_kernel(const PagedArgs a, PromptUnit* units, int grid, int tiles, int target,
+                         int min_rows) {
   __shared__ long long s_sum[kThreads / 32];
   __shared__ int2 s_scan[kThreads / 32];
-  __shared__ int s_unit[7];
+  __shared__ int2 s_len[kSorted];
+  __shared__ int s_starts[kMaxStagedSeqs];
+  grid_dependency_wait();
+  grid_launch_dependents();
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int* starts = a.q_start;
   if (a.B <= kMaxStagedSeqs) {
-    int* staged = reinterpret_cast<int*>(scratch);
-    for (int i = tid; i < a.B; i += kThreads) staged[i] = a.q_start[i];
-    starts = staged;
+    for (int i = tid; i < a.B; i += kThreads) s_starts[i] = a.q_start[i];
+    starts = s_starts;
   }
-  if (tid == 0) s_unit[0] = -1;
   __syncthreads();
   int b0 = 0, row0 = 0, n0 = -1;
   long long sum = 0;
@@ -341,12 +348,14 @@ __device__ __forceinline__ Unit find_unit(const PagedArgs& a, int tiles, int tar
   for (int w = 0; w < kThreads / 32; ++w) sum += s_sum[w];
   const long long want = (sum * a.Hkv + target - 1) / target;
   const int chunk = static_cast<int>(want < kMinChunk ? kMinChunk : want);
+  const bool sorted = tiles <= kSorted;
   int base = 0, pbase = 0;
-  for (int s0 = 0; s0 < tiles && base <= static_cast<int>(blockIdx.x); s0 += kThreads) {
+  for (int s0 = 0; s0 < tiles; s0 += kThreads) {
     const int s = s0 + tid;
     int n = n0, b = b0, r = row0;
     if (s0 > 0) n = s < tiles ? slot_steps(a, tiles - 1 - s, min_rows, starts, b, r) : -1;
     const int nsplit = n < 0 ? 0 : (n <= chunk ? 1 : (n + chunk - 1) / chunk);
+    const int per = nsplit > 0 ? (n + nsplit - 1) / nsplit : 0;      // splits are equally long
     const int mine = nsplit * a.Hkv, parts = nsplit > 1 ? mine : 0;
     int incl = mine, pincl = parts;
 #pragma unroll
@@ -359,47 +368,48 @@ __device__ __forceinline__ Unit find_unit(const PagedArgs& a, int tiles, int tar
       }
     }
     if (lane == 31) s_scan[warp] = make_int2(incl, pincl);
+    if (sorted && tid < kSorted) s_len[tid] = make_int2(nsplit > 0 ? per : -1, mine);
     __syncthreads();
-    int before = base, pbefore = pbase;
+    int first = base + incl - mine, part = pbase + pincl - parts;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
       if (w < warp) {
-        before += s_scan[w].x;
-        pbefore += s_scan[w].y;
+        first += s_scan[w].x;
+        part += s_scan[w].y;
       }
       base += s_scan[w].x;
       pbase += s_scan[w].y;
     }
-    const int off = static_cast<int>(blockIdx.x) - (before + incl - mine);
-    if (off >= 0 && off < mine) {
-      s_unit[0] = b;
-      s_unit[1] = r;
-      s_unit[2] = off;
-      s_unit[3] = nsplit;
-      s_unit[4] = tiles - 1 - s;
-      s_unit[5] = n;
-      s_unit[6] = pbefore + pincl - parts + off;
+    if (sorted && mine > 0) {
+      first = 0;
+      for (int i = 0; i < tiles; ++i) {
+        const int2 o = s_len[i];
+        first += o.x > per || (o.x == per && i < tid) ? o.y : 0;
+      }
+    }
+    if (s < tiles && a.meta != nullptr)
+      for (int hk = 0; hk < a.Hkv; ++hk)
+        a.meta[(tiles - 1 - s) * a.Hkv + hk] =
+            make_int2(nsplit > 1 ? part + hk * nsplit : 0, nsplit);
+    for (int i = 0; i < mine; ++i) {
+      PromptUnit u;
+      u.b = b;
+      u.row0 = r;
+      u.hk = i / nsplit;
+      u.whole = nsplit == 1;
+      u.step0 = (i - u.hk * nsplit) * per;
+      u.step1 = u.step0 + per < n ? u.step0 + per : n;
+      u.part = part + i;
+      u.unused = 0;
+      if (first + i < grid) units[first + i] = u;
     }
     __syncthreads();
   }
-  Unit u;
-  u.b = s_unit[0];
-  if (u.b < 0) return u;
-  u.row0 = s_unit[1];
-  u.nsplit = s_unit[3];
-  u.hk = s_unit[2] / u.nsplit;
-  u.split = s_unit[2] - u.hk * u.nsplit;
-  u.slot = s_unit[4];
-  u.part = s_unit[6];
-  // splits of one slot are equally long
-  const int per = (s_unit[5] + u.nsplit - 1) / u.nsplit;
-  u.step0 = u.split * per;
-  u.step1 = u.step0 + per < s_unit[5] ? u.step0 + per : s_unit[5];
-  return u;
+  for (int i = base + tid; i < grid; i += kThreads) units[i].b = -1;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
-paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
+paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
   extern __shared__ uint8_t raw[];
   __shared__ Bars bars;
   __shared__ uint32_t s_tmem;
@@ -413,7 +423,7 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
   const uint32_t s0 = smem_u32(smem);
   grid_dependency_wait();
   grid_launch_dependents();
-  const Unit u = find_unit(a, tiles, target, min_rows, smem);
+  const PromptUnit u = units[blockIdx.x];
   if (u.b < 0) return;
 
   const RowRange rr = rows_of(a.q_start, u.b, a.T);
@@ -666,7 +676,7 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
       if (steps > 0 && ok) ok = wait(bars.o_full, 0, kErrEpilogue);
       if (ok) {
         tc_fence_after_sync();
-        const bool whole = u.nsplit == 1;
+        const bool whole = u.whole;
         // (a row that saw no token has l = 0; its O is zero or was not written)
         const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
         const int rows0 = u.row0 + kTile * x + 32 * (warp & 3);      // the warp's first row
@@ -725,8 +735,6 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
         }
       }
     }
-    if (tid == 0 && u.split == 0 && a.meta != nullptr)
-      a.meta[u.slot * a.Hkv + u.hk] = make_int2(u.part, u.nsplit);
   } else if (warp < 12) {
     // --------------------------------------------------------------- producer
     regs_dec<96>();
@@ -914,17 +922,17 @@ paged_prompt_kernel(const PagedArgs a, int tiles, int target, int min_rows) {
 // row at a time.
 constexpr int kCombineRows = 32;
 __global__ void __launch_bounds__(256)
-paged_prompt_combine_kernel(const PagedArgs a, int tiles, int min_rows) {
+paged_prompt_combine_kernel(const PagedArgs a, int min_rows) {
   grid_dependency_wait();
   grid_launch_dependents();
   constexpr int kParts = kSlotRows / kCombineRows;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int pair = blockIdx.x / kParts;
   const int slot = pair / a.Hkv, hk = pair - slot * a.Hkv;
-  int b = 0, row0 = 0;
-  if (slot_steps(a, slot, min_rows, a.q_start, b, row0) <= kMinChunk) return;   // not split
   const int2 mt = a.meta[pair];
-  if (mt.y <= 1) return;
+  if (mt.y <= 1) return;                   // no work, or not split
+  int b = 0, row0 = 0;
+  slot_steps(a, slot, min_rows, a.q_start, b, row0);
   const RowRange rr = rows_of(a.q_start, b, a.T);
   for (int i = warp; i < kCombineRows; i += 8) {
     const int rs = (blockIdx.x - pair * kParts) * kCombineRows + i;
@@ -932,23 +940,36 @@ paged_prompt_combine_kernel(const PagedArgs a, int tiles, int min_rows) {
     if (r >= rr.n * a.g) return;
     const float* base = a.parts + (static_cast<size_t>(mt.x) * kSlotRows + rs) * kPartFloats;
     const size_t step = static_cast<size_t>(kSlotRows) * kPartFloats;
-    float M = -INFINITY;
-    for (int p = lane; p < mt.y; p += 32) M = fmaxf(M, base[p * step]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float den = 0.0f;
+    float M = -INFINITY, den = 0.0f;
     float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int p = 0; p < mt.y; ++p) {
-      const float* pp = base + p * step;
-      const float m = pp[0];
-      const float f = m == -INFINITY ? 0.0f : fast_exp2(m - M);
-      const float4 v = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
-      den += f * pp[1];
-      num.x += f * v.x;
-      num.y += f * v.y;
-      num.z += f * v.z;
-      num.w += f * v.w;
+    for (int p0 = 0; p0 < mt.y; p0 += 4) {     // four parts at a time, loaded together
+      float m[4], l[4];
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* pp = base + (p0 + i < mt.y ? p0 + i : p0) * step;
+        m[i] = p0 + i < mt.y ? pp[0] : -INFINITY;
+        l[i] = pp[1];
+        v[i] = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
+      }
+      const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
+      const float al = M == -INFINITY ? 0.0f : fast_exp2(M - top);
+      M = top;
+      den *= al;
+      num.x *= al;
+      num.y *= al;
+      num.z *= al;
+      num.w *= al;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = m[i] == -INFINITY ? 0.0f : fast_exp2(m[i] - top);
+        if (f == 0.0f) continue;
+        den += f * l[i];
+        num.x += f * v[i].x;
+        num.y += f * v[i].y;
+        num.z += f * v[i].z;
+        num.w += f * v[i].w;
+      }
     }
     const int qi = r / a.g;
     store_row4(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g + (r - qi * a.g)) *
@@ -977,6 +998,7 @@ void plan_prompt(PagedPlan& p, int T, int B, int Hq, int Hkv, int width, int pag
   // n / chunk + 1 < 2 n / chunk units, and the batch at most 2 target of them)
   const long long units = p.prompt_target + pairs, all = pairs * most_splits;
   p.prompt_grid = static_cast<int>(units < all ? units : all);
+  p.prompt_units_off = p.take(static_cast<size_t>(p.prompt_grid) * sizeof(PromptUnit));
   if (most_splits > 1) {
     const long long split = 2LL * p.prompt_target;
     const long long parts = split < p.prompt_grid ? split : p.prompt_grid;
@@ -987,15 +1009,20 @@ void plan_prompt(PagedPlan& p, int T, int B, int Hq, int Hkv, int width, int pag
   }
 }
 
-int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, cudaStream_t s) {
+int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, void* units,
+                        cudaStream_t s) {
   if (int st = prepare_prompt_kernel()) return st;
+  PromptUnit* list = static_cast<PromptUnit*>(units);
+  if (int st = launch_dependent(paged_prompt_plan_kernel, dim3(1), kThreads, 0, s, a, list,
+                                p.prompt_grid, p.tiles, p.prompt_target, min_rows))
+    return st;
   if (int st = launch_dependent(paged_prompt_kernel, dim3(static_cast<unsigned>(p.prompt_grid)),
-                                kThreads, kSmemBytes, s, a, p.tiles, p.prompt_target, min_rows))
+                                kThreads, kSmemBytes, s, a, static_cast<const PromptUnit*>(list)))
     return st;
   if (!p.prompt_combine) return QOQ_OK;
   const long long ctas = static_cast<long long>(p.tiles) * a.Hkv * (kSlotRows / kCombineRows);
   return launch_dependent(paged_prompt_combine_kernel, dim3(static_cast<unsigned>(ctas)), 256, 0, s,
-                          a, p.tiles, min_rows);
+                          a, min_rows);
 }
 
 int prompt_device_error(unsigned int* value, int clear) {
