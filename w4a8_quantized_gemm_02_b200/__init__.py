@@ -487,35 +487,47 @@ def _on(t, stream):
     return stack
 
 
+_torch = None
+
+
+def _load_torch():
+    """torch, imported at the first call that needs it."""
+    global _torch
+    import torch
+    _torch = torch
+    return torch
+
+
 def _elsewhere(t, stream):
     """Whether a call on `t` is not simply one on the current device's current
     stream.  Such a call is made again inside _on, so that its outputs and
     workspace belong to the stream it runs on."""
-    import torch
-    return stream is not None or t.get_device() != torch.cuda.current_device()
+    return stream is not None or t.get_device() != _torch.cuda.current_device()
 
 
 def _current_stream(device: int) -> int:
     """The address of a device's current stream."""
-    import torch
     try:
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _torch._C._cuda_getCurrentRawStream(device)
     except AttributeError:   # the public way, which takes 20 times as long
-        return torch.cuda.current_stream(device).cuda_stream
+        return _torch.cuda.current_stream(device).cuda_stream
 
 
 def _need(t, name, dtype, shape, dev):
-    """_need_cuda of a dtype, shape and device, quick for a tensor that has
+    """_need_cuda of a dtype, shape and CUDA device, quick for a tensor that has
     them: these calls take a few microseconds on the device."""
-    if not (getattr(t, "dtype", None) is dtype and t.device == dev and t.shape == shape
-            and t.is_contiguous() and t.is_cuda):
-        _need_cuda(t, name, dtype, shape=shape, device=dev)
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
+            return
+    except AttributeError:
+        pass
+    _need_cuda(t, name, dtype, shape=shape, device=dev)
 
 
 def _need_rows(t, name, dtype, width, device=None):
     """A CUDA tensor of rows of `width` contiguous elements, the rows any
     multiple of 16 bytes apart; returns (rows, elements between rows)."""
-    import torch
+    torch = _torch
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
@@ -540,7 +552,7 @@ def _need_rows(t, name, dtype, width, device=None):
 
 def _need_batch(cache, q_start, seqlen, block_table, dev):
     """Checks a paged cache and a ragged batch; returns (pages, Hkv, page, B, width)."""
-    import torch
+    torch = _torch
     kc, vc, sc = cache
     shape = getattr(sc, "shape", ())
     if len(shape) != 4 or shape[3] != 4 or shape[2] % 16:
@@ -662,7 +674,7 @@ def kv4_paged_append(qkv, cache, q_start, seqlen, block_table, Hq: int, inv_freq
     int32.  inv_freq: float64 (rot / 2) from rope_frequencies (None: no
     rotation), rope_layout "half" or "interleaved".  values: (K, V), each
     (T, Hkv, 128) float16, written with the values that the cache then holds."""
-    import torch
+    torch = _torch or _load_torch()
     if rope_layout not in _ROPE_LAYOUTS:
         raise ValueError(f"rope_layout must be one of {sorted(_ROPE_LAYOUTS)}")
     if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda:
@@ -684,7 +696,7 @@ def kv4_paged_append(qkv, cache, q_start, seqlen, block_table, Hq: int, inv_freq
         _need(vh, "values[1]", torch.float16, (T, Hkv, 128), dev)
         k_at, v_at = kh.data_ptr(), vh.data_ptr()
     if q_out is None:
-        q_out = torch.empty((T, Hq, 128), dtype=torch.float16, device=dev)
+        q_out = qkv.new_empty((T, Hq, 128))
     else:
         _need(q_out, "q_out", torch.float16, (T, Hq, 128), dev)
     st = lib().qoq_kv4_paged_append(
@@ -706,7 +718,7 @@ def kv4_paged_attention(Q, cache, q_start, seqlen, block_table, max_q=None, scal
     number of rows of a sequence (1 for a decode step; default: T).  scale:
     default 1 / sqrt(128).  ws: a uint8 workspace of
     kv4_paged_attention_workspace_bytes (default: allocated for the call)."""
-    import torch
+    torch = _torch or _load_torch()
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.shape[2] != 128:
         raise ValueError("Q must have shape (T, Hq, 128)")
     if not Q.is_cuda:
@@ -721,12 +733,11 @@ def kv4_paged_attention(Q, cache, q_start, seqlen, block_table, max_q=None, scal
     max_q = max(T, 1) if max_q is None else max_q
     scale = _DEFAULT_SCALE if scale is None else scale
     if out is None:
-        out = torch.empty((T, Hq, 128), dtype=torch.float16, device=dev)
+        out = Q.new_empty((T, Hq, 128))
     else:
         _need(out, "out", torch.float16, (T, Hq, 128), dev)
     if ws is None:
-        ws = torch.empty(_attention_ws(dev.index, T, Hq, Hkv, B, width, page, max_q),
-                         dtype=torch.uint8, device=dev)
+        ws = cache[0].new_empty(_attention_ws(dev.index, T, Hq, Hkv, B, width, page, max_q))
     else:
         _need_ws(ws, dev)
     st = lib().qoq_kv4_paged_attention(
@@ -943,7 +954,7 @@ def lora_add(Y, X, A, B, ids, scaling, out=None, ws=None, stream=None):
     Y (T, N), X (T, K), A (n, R, K), B (n, N, R) float16, ids (T,) int32,
     scaling (n,) float32.  out: a (T, N) float16 tensor, which may be Y
     (default: a new one)."""
-    import torch
+    torch = _torch or _load_torch()
     if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2:
         raise ValueError("X must be a CUDA tensor with 2 dims")
     if _elsewhere(X, stream):
@@ -961,7 +972,7 @@ def lora_add(Y, X, A, B, ids, scaling, out=None, ws=None, stream=None):
     _need(ids, "ids", torch.int32, (T,), dev)
     _need(scaling, "scaling", torch.float32, (n,), dev)
     if out is None:
-        out = torch.empty((T, N), dtype=torch.float16, device=dev)
+        out = torch.empty_like(Y)
     elif out is not Y:
         _need(out, "out", torch.float16, (T, N), dev)
     if ws is None:
