@@ -48,8 +48,8 @@ struct PagedPlan {
 PagedPlan paged_plan(int T, int B, int Hq, int Hkv, int width, int page, int max_q);
 void plan_prompt(PagedPlan& p, int T, int B, int Hq, int Hkv, int width, int page);
 
-// `units`: the workspace's list of units.
-int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, void* units,
+struct PromptUnit;
+int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, const PromptUnit* units,
                         cudaStream_t s);
 
 // 4 or 8 outputs times `f`, rounded to FP16.

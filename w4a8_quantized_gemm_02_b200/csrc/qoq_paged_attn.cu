@@ -44,6 +44,7 @@
 #include "qoq_internal.h"
 #include "qoq_kv4.cuh"
 #include "qoq_paged.h"
+#include "qoq_prompt_plan.cuh"
 
 namespace qoq {
 namespace {
@@ -96,10 +97,11 @@ __device__ __forceinline__ int weight_of(int blocks) {
   return blocks < 0 ? 0 : kPairCost + (blocks == 0 ? 1 : blocks);
 }
 
-// Grid: one CTA for each that is resident.
+// Grid: `ctas` CTAs, one for each that is resident, and one more where there may be
+// prompt chunks, which lists their units.
 template <int NT>
 __global__ void __launch_bounds__(kThreads, resident_ctas(NT))
-paged_decode_kernel(const PagedArgs a) {
+paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
   constexpr int kRows = 4 * NT;
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ long long s_sum[kWarps], s_start;
@@ -108,6 +110,11 @@ paged_decode_kernel(const PagedArgs a) {
   const int gid = lane >> 2, tig = lane & 3;
   grid_dependency_wait();
   grid_launch_dependents();
+  if (static_cast<int>(blockIdx.x) == ctas) {
+    static_assert(kPlanScratch <= kWarps * kStages * kStageBytes, "scratch");
+    list_prompt_units<kThreads>(a, pp, smem);
+    return;
+  }
 
   // --- this CTA's run: [start, end) of the batch's `total` blocks ---
   // (counted with it: the sequences that have work, in the upper bits)
@@ -131,7 +138,7 @@ paged_decode_kernel(const PagedArgs a) {
   // at least kPairCost + kMinBlocks, but no more than the mean pair: short ones have
   // a CTA each
   const long long mean = (sum + active - 1) / active;
-  long long run = (total + gridDim.x - 1) / gridDim.x;
+  long long run = (total + ctas - 1) / ctas;
   const long long least = mean < kPairCost + kMinBlocks ? mean : kPairCost + kMinBlocks;
   if (run < least) run = least;
   const long long start = run * blockIdx.x;
@@ -511,14 +518,86 @@ paged_decode_kernel(const PagedArgs a) {
   }
 }
 
-// The rows of the split sequences from their partial results, W warps a row:
-// a warp takes every W-th split, a lane four dimensions.
+// A list of units where no decode kernel runs.
+__global__ void __launch_bounds__(kThreads) prompt_plan_kernel(const PagedArgs a, const PromptPlan pp) {
+  __shared__ __align__(16) uint8_t scratch[kPlanScratch];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  list_prompt_units<kThreads>(a, pp, scratch);
+}
+
+// Rows of a split slot from their partial results: kCombineRows rows a CTA (number `cta`),
+// a warp a row at a time.
+constexpr int kCombineRows = 32;
+__device__ __forceinline__ void merge_slot(const PagedArgs& a, const PromptPlan& pp,
+                                           const float* parts, int cta) {
+  constexpr int kParts = kSlotRows / kCombineRows;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int pair = cta / kParts;
+  const int slot = pair / a.Hkv, hk = pair - slot * a.Hkv;
+  const int2 mt = pp.meta[pair];
+  if (mt.y <= 1) return;                   // no work, or not split
+  int b = 0, row0 = 0;
+  slot_steps(a, slot, pp.min_rows, a.q_start, b, row0);
+  const RowRange rr = rows_of(a.q_start, b, a.T);
+  for (int i = warp; i < kCombineRows; i += 8) {
+    const int rs = (cta - pair * kParts) * kCombineRows + i;
+    const int r = row0 + rs;
+    if (r >= rr.n * a.g) return;
+    const float* base = parts + (static_cast<size_t>(mt.x) * kSlotRows + rs) * kPartFloats;
+    const size_t step = static_cast<size_t>(kSlotRows) * kPartFloats;
+    float M = -INFINITY, den = 0.0f;
+    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int p0 = 0; p0 < mt.y; p0 += 4) {     // four parts at a time, loaded together
+      float m[4], l[4];
+      float4 v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float* pp = base + (p0 + i < mt.y ? p0 + i : p0) * step;
+        m[i] = p0 + i < mt.y ? pp[0] : -INFINITY;
+        l[i] = pp[1];
+        v[i] = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
+      }
+      const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
+      const float al = M == -INFINITY ? 0.0f : fast_exp2(M - top);
+      M = top;
+      den *= al;
+      num.x *= al;
+      num.y *= al;
+      num.z *= al;
+      num.w *= al;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = m[i] == -INFINITY ? 0.0f : fast_exp2(m[i] - top);
+        if (f == 0.0f) continue;
+        den += f * l[i];
+        num.x += f * v[i].x;
+        num.y += f * v[i].y;
+        num.z += f * v[i].z;
+        num.w += f * v[i].w;
+      }
+    }
+    const int qi = r / a.g;
+    store_row4(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g + (r - qi * a.g)) *
+                           kHeadDim + 4 * lane, num, den == 0.0f ? 0.0f : __frcp_rn(den));
+  }
+}
+
+// The merge: CTAs up to `decode_ctas` take rows of the decode kernel's split pairs, W
+// warps a row (a warp every W-th part, a lane four dimensions), the others rows of the
+// prompt kernel's split slots.
 template <int W>
-__global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a, int rows, int stride) {
+__global__ void __launch_bounds__(256)
+paged_combine_kernel(const PagedArgs a, int rows, int stride, int decode_ctas, const PromptPlan pp,
+                     const float* prompt_parts) {
   __shared__ float4 red_num[8][32];
   __shared__ float2 red_md[8];
   grid_dependency_wait();
   grid_launch_dependents();
+  if (static_cast<int>(blockIdx.x) >= decode_ctas) {
+    merge_slot(a, pp, prompt_parts, blockIdx.x - decode_ctas);
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int sub = warp % W;
   const long long x = static_cast<long long>(blockIdx.x) * (8 / W) + warp / W;
@@ -582,23 +661,31 @@ __global__ void __launch_bounds__(256) paged_combine_kernel(const PagedArgs a, i
 }
 
 template <int NT>
-int launch_decode(const PagedArgs& a, const PagedPlan& p, cudaStream_t s) {
+int launch_decode(const PagedArgs& a, const PagedPlan& p, const PromptPlan& pp, cudaStream_t s) {
   constexpr size_t smem = static_cast<size_t>(kWarps) * kStages * kStageBytes;
   static std::atomic<unsigned long long> ready{0};
   if (int st = opt_in_smem(reinterpret_cast<const void*>(paged_decode_kernel<NT>), smem, ready))
     return st;
-  if (int st = launch_dependent(paged_decode_kernel<NT>, dim3(static_cast<unsigned>(p.grid)),
-                                kThreads, smem, s, a))
-    return st;
-  if (!p.combine) return QOQ_OK;
-  const int rows = a.max_q * a.g < 4 * NT ? a.max_q * a.g : 4 * NT;
-  const long long all = static_cast<long long>(a.B) * a.Hkv * rows;
+  return launch_dependent(paged_decode_kernel<NT>,
+                          dim3(static_cast<unsigned>(p.grid + (pp.units ? 1 : 0))), kThreads, smem,
+                          s, a, p.grid, pp);
+}
+
+int launch_combine(const PagedArgs& a, const PagedPlan& p, const PromptPlan& pp,
+                   const float* prompt_parts, cudaStream_t s) {
+  const int rows = a.max_q * a.g < 4 * p.nt ? a.max_q * a.g : 4 * p.nt;
+  const long long all = p.combine ? static_cast<long long>(a.B) * a.Hkv * rows : 0;
+  const long long prompt = p.prompt && p.prompt_combine
+                               ? static_cast<long long>(p.tiles) * a.Hkv * (kSlotRows / kCombineRows)
+                               : 0;
+  if (all + prompt == 0) return QOQ_OK;
   // few rows have many parts each: eight warps a row
   if (all <= 512)
-    return launch_dependent(paged_combine_kernel<8>, dim3(static_cast<unsigned>(all)), 256, 0, s, a,
-                            rows, 4 * NT);
-  return launch_dependent(paged_combine_kernel<1>, dim3(static_cast<unsigned>((all + 7) / 8)), 256,
-                          0, s, a, rows, 4 * NT);
+    return launch_dependent(paged_combine_kernel<8>, dim3(static_cast<unsigned>(all + prompt)), 256,
+                            0, s, a, rows, 4 * p.nt, static_cast<int>(all), pp, prompt_parts);
+  const long long ctas = (all + 7) / 8;
+  return launch_dependent(paged_combine_kernel<1>, dim3(static_cast<unsigned>(ctas + prompt)), 256, 0,
+                          s, a, rows, 4 * p.nt, static_cast<int>(ctas), pp, prompt_parts);
 }
 
 }  // namespace
@@ -689,17 +776,29 @@ extern "C" int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq,
   a.out = static_cast<__half*>(out);
   char* w = static_cast<char*>(ws);
   cudaStream_t s = as_stream(stream);
-  if (p.nt) {
-    a.meta = p.combine ? reinterpret_cast<int2*>(w + p.meta_off) : nullptr;
-    a.parts = p.combine ? reinterpret_cast<float*>(w + p.parts_off) : nullptr;
-    const int st = p.nt == 1 ? launch_decode<1>(a, p, s)
-                             : (p.nt == 2 ? launch_decode<2>(a, p, s) : launch_decode<4>(a, p, s));
-    if (st) return st;
-  }
+  PromptPlan pp = {};
   if (p.prompt) {
-    a.meta = p.prompt_combine ? reinterpret_cast<int2*>(w + p.prompt_meta_off) : nullptr;
-    a.parts = p.prompt_combine ? reinterpret_cast<float*>(w + p.prompt_parts_off) : nullptr;
-    return launch_paged_prompt(a, p, 4 * p.nt + 1, w + p.prompt_units_off, s);
+    pp.units = reinterpret_cast<PromptUnit*>(w + p.prompt_units_off);
+    pp.meta = p.prompt_combine ? reinterpret_cast<int2*>(w + p.prompt_meta_off) : nullptr;
+    pp.grid = p.prompt_grid;
+    pp.tiles = p.tiles;
+    pp.target = p.prompt_target;
+    pp.min_rows = 4 * p.nt + 1;
   }
-  return QOQ_OK;
+  a.meta = p.combine ? reinterpret_cast<int2*>(w + p.meta_off) : nullptr;
+  a.parts = p.combine ? reinterpret_cast<float*>(w + p.parts_off) : nullptr;
+  int st = QOQ_OK;
+  if (p.nt == 1) st = launch_decode<1>(a, p, pp, s);
+  else if (p.nt == 2) st = launch_decode<2>(a, p, pp, s);
+  else if (p.nt == 4) st = launch_decode<4>(a, p, pp, s);
+  else st = launch_dependent(prompt_plan_kernel, dim3(1), kThreads, 0, s, a, pp);
+  if (st) return st;
+  float* prompt_parts = nullptr;
+  if (p.prompt) {
+    PagedArgs b = a;
+    prompt_parts = p.prompt_combine ? reinterpret_cast<float*>(w + p.prompt_parts_off) : nullptr;
+    b.parts = prompt_parts;
+    if (int e = launch_paged_prompt(b, p, pp.units, s)) return e;
+  }
+  return launch_combine(a, p, pp, prompt_parts, s);
 }

@@ -27,9 +27,9 @@
 // are the k index of W V, are token position 8 tig + 4 block + 2 j1 + e of each 32
 // (the rows of the K tile are stored at them).  Every store is 16 bytes.
 //
-// Splits.  A kernel of one CTA ahead of it looks the lengths over and lists the units
-// of work: long sequences with few rows are split so that no CTA is left with a long
-// one, and a last kernel merges.
+// Splits.  One CTA of the kernel ahead looks the lengths over and lists the units of
+// work: long sequences with few rows are split so that no CTA is left with a long one,
+// and a last kernel merges.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <math.h>
@@ -42,6 +42,7 @@
 #include "qoq_internal.h"
 #include "qoq_kv4.cuh"
 #include "qoq_paged.h"
+#include "qoq_prompt_plan.cuh"
 
 namespace qoq {
 
@@ -52,14 +53,10 @@ namespace {
 __device__ unsigned int g_prompt_error = 0;
 
 constexpr int kThreads = 512;
-constexpr int kSlotRows = 256;
-constexpr int kTile = 128;                      // rows of a tile, tokens of a step
-constexpr int kMinChunk = 8;                    // steps: a split's least length
+constexpr int kTile = kStepTokens;              // rows of a tile, tokens of a step
 constexpr float kRaise = 2.9f;                  // 2^2.9 * 131008 / 15 is an FP16 number
 constexpr float kHeadroom = 2.0f;               // a raised reference lies this far above the
                                                 // score: a raise rescales O, and one is enough
-constexpr int kMaxStagedSeqs = 2048;
-constexpr int kSorted = 256;                    // slots up to which units go by length
 
 // Shared memory: Q 2 tiles x 2 halves of 64 dimensions x [128 rows][128 bytes],
 // K and V twice each, 2 halves x [128][128 bytes] (128-byte swizzle).
@@ -272,140 +269,6 @@ __device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity,
       return false;
     }
   }
-}
-
-// A unit of work: steps step0 .. step1 - 1 (of 128 tokens) for the slot of rows from
-// row0 on of sequence b (-1: nothing) and KV head hk.
-struct __align__(16) PromptUnit {
-  int b, row0, hk;
-  int whole;         // the slot is not split
-  int step0, step1;
-  int part;          // its number among the units of split slots
-  int unused;
-};
-
-// Steps of slot `slot` (128-token steps that its last row sees), -1 for a slot
-// without work here; b and the first row of it.
-__device__ __forceinline__ int slot_steps(const PagedArgs& a, int slot, int min_rows,
-                                          const int* starts, int& b, int& row0) {
-  int lo = 0, hi = a.B;        // the last sequence whose slots start at or before this one
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (slot_base(starts[mid], mid, a.g, kSlotRows) <= slot) lo = mid;
-    else hi = mid;
-  }
-  b = lo;
-  const RowRange rr = rows_of(a.q_start, lo, a.T);
-  const int R = rr.n * a.g;
-  const long long first =
-      static_cast<long long>(slot - slot_base(rr.first, lo, a.g, kSlotRows)) * kSlotRows;
-  if (rr.n <= 0 || rr.n > a.max_q || R < min_rows || first < 0 || first >= R) return -1;
-  row0 = static_cast<int>(first);
-  const int last = (row0 + kSlotRows < R ? row0 + kSlotRows : R) - 1;
-  const int len = clamp_len(a.seqlen[lo], a.width * a.page);
-  return (visible(position_of(a.seqlen[lo], rr.n, last / a.g), len) + kTile - 1) / kTile;
-}
-
-// The list of units, one CTA.  Splits are equally long over the whole batch: the
-// batch's steps over `target`, kMinChunk at least.  Units go by length where the slots
-// are few (the CTAs that come last should be the shortest), else the last slots, which
-// see most, come first.  meta: per (slot, KV head) its first part and their number, 0
-// for a slot without work and 1 for a whole one.
-__global__ void __launch_bounds__(kThreads)
-paged_prompt_plan_kernel(const PagedArgs a, PromptUnit* units, int grid, int tiles, int target,
-                         int min_rows) {
-  __shared__ long long s_sum[kThreads / 32];
-  __shared__ int2 s_scan[kThreads / 32];
-  __shared__ int2 s_len[kSorted];
-  __shared__ int s_starts[kMaxStagedSeqs];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int* starts = a.q_start;
-  if (a.B <= kMaxStagedSeqs) {
-    for (int i = tid; i < a.B; i += kThreads) s_starts[i] = a.q_start[i];
-    starts = s_starts;
-  }
-  __syncthreads();
-  int b0 = 0, row0 = 0, n0 = -1;
-  long long sum = 0;
-  for (int s = tid; s < tiles; s += kThreads) {
-    int b = 0, r = 0;
-    const int n = slot_steps(a, tiles - 1 - s, min_rows, starts, b, r);
-    if (s == tid) {
-      n0 = n;
-      b0 = b;
-      row0 = r;
-    }
-    if (n > 0) sum += n;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if (lane == 0) s_sum[warp] = sum;
-  __syncthreads();
-  sum = 0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) sum += s_sum[w];
-  const long long want = (sum * a.Hkv + target - 1) / target;
-  const int chunk = static_cast<int>(want < kMinChunk ? kMinChunk : want);
-  const bool sorted = tiles <= kSorted;
-  int base = 0, pbase = 0;
-  for (int s0 = 0; s0 < tiles; s0 += kThreads) {
-    const int s = s0 + tid;
-    int n = n0, b = b0, r = row0;
-    if (s0 > 0) n = s < tiles ? slot_steps(a, tiles - 1 - s, min_rows, starts, b, r) : -1;
-    const int nsplit = n < 0 ? 0 : (n <= chunk ? 1 : (n + chunk - 1) / chunk);
-    const int per = nsplit > 0 ? (n + nsplit - 1) / nsplit : 0;      // splits are equally long
-    const int mine = nsplit * a.Hkv, parts = nsplit > 1 ? mine : 0;
-    int incl = mine, pincl = parts;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, incl, o);
-      const int pup = __shfl_up_sync(0xffffffffu, pincl, o);
-      if (lane >= o) {
-        incl += up;
-        pincl += pup;
-      }
-    }
-    if (lane == 31) s_scan[warp] = make_int2(incl, pincl);
-    if (sorted && tid < kSorted) s_len[tid] = make_int2(nsplit > 0 ? per : -1, mine);
-    __syncthreads();
-    int first = base + incl - mine, part = pbase + pincl - parts;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) {
-        first += s_scan[w].x;
-        part += s_scan[w].y;
-      }
-      base += s_scan[w].x;
-      pbase += s_scan[w].y;
-    }
-    if (sorted && mine > 0) {
-      first = 0;
-      for (int i = 0; i < tiles; ++i) {
-        const int2 o = s_len[i];
-        first += o.x > per || (o.x == per && i < tid) ? o.y : 0;
-      }
-    }
-    if (s < tiles && a.meta != nullptr)
-      for (int hk = 0; hk < a.Hkv; ++hk)
-        a.meta[(tiles - 1 - s) * a.Hkv + hk] =
-            make_int2(nsplit > 1 ? part + hk * nsplit : 0, nsplit);
-    for (int i = 0; i < mine; ++i) {
-      PromptUnit u;
-      u.b = b;
-      u.row0 = r;
-      u.hk = i / nsplit;
-      u.whole = nsplit == 1;
-      u.step0 = (i - u.hk * nsplit) * per;
-      u.step1 = u.step0 + per < n ? u.step0 + per : n;
-      u.part = part + i;
-      u.unused = 0;
-      if (first + i < grid) units[first + i] = u;
-    }
-    __syncthreads();
-  }
-  for (int i = base + tid; i < grid; i += kThreads) units[i].b = -1;
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -918,65 +781,6 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
   if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-// Rows of the split slots from their partial results: kCombineRows rows a CTA, a warp a
-// row at a time.
-constexpr int kCombineRows = 32;
-__global__ void __launch_bounds__(256)
-paged_prompt_combine_kernel(const PagedArgs a, int min_rows) {
-  grid_dependency_wait();
-  grid_launch_dependents();
-  constexpr int kParts = kSlotRows / kCombineRows;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int pair = blockIdx.x / kParts;
-  const int slot = pair / a.Hkv, hk = pair - slot * a.Hkv;
-  const int2 mt = a.meta[pair];
-  if (mt.y <= 1) return;                   // no work, or not split
-  int b = 0, row0 = 0;
-  slot_steps(a, slot, min_rows, a.q_start, b, row0);
-  const RowRange rr = rows_of(a.q_start, b, a.T);
-  for (int i = warp; i < kCombineRows; i += 8) {
-    const int rs = (blockIdx.x - pair * kParts) * kCombineRows + i;
-    const int r = row0 + rs;
-    if (r >= rr.n * a.g) return;
-    const float* base = a.parts + (static_cast<size_t>(mt.x) * kSlotRows + rs) * kPartFloats;
-    const size_t step = static_cast<size_t>(kSlotRows) * kPartFloats;
-    float M = -INFINITY, den = 0.0f;
-    float4 num = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    for (int p0 = 0; p0 < mt.y; p0 += 4) {     // four parts at a time, loaded together
-      float m[4], l[4];
-      float4 v[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float* pp = base + (p0 + i < mt.y ? p0 + i : p0) * step;
-        m[i] = p0 + i < mt.y ? pp[0] : -INFINITY;
-        l[i] = pp[1];
-        v[i] = *reinterpret_cast<const float4*>(pp + 4 + 4 * lane);
-      }
-      const float top = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), M);
-      const float al = M == -INFINITY ? 0.0f : fast_exp2(M - top);
-      M = top;
-      den *= al;
-      num.x *= al;
-      num.y *= al;
-      num.z *= al;
-      num.w *= al;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float f = m[i] == -INFINITY ? 0.0f : fast_exp2(m[i] - top);
-        if (f == 0.0f) continue;
-        den += f * l[i];
-        num.x += f * v[i].x;
-        num.y += f * v[i].y;
-        num.z += f * v[i].z;
-        num.w += f * v[i].w;
-      }
-    }
-    const int qi = r / a.g;
-    store_row4(a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + hk * a.g + (r - qi * a.g)) *
-                           kHeadDim + 4 * lane, num, den == 0.0f ? 0.0f : __frcp_rn(den));
-  }
-}
-
 // Once per device: opt in to the shared memory, and check the registers.  The
 // kernel's warpgroups split 4 x 128 a thread among them (168, 168, 96, 80); a
 // launch with fewer would wait for registers that never come free.
@@ -1009,20 +813,11 @@ void plan_prompt(PagedPlan& p, int T, int B, int Hq, int Hkv, int width, int pag
   }
 }
 
-int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, int min_rows, void* units,
+int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, const PromptUnit* units,
                         cudaStream_t s) {
   if (int st = prepare_prompt_kernel()) return st;
-  PromptUnit* list = static_cast<PromptUnit*>(units);
-  if (int st = launch_dependent(paged_prompt_plan_kernel, dim3(1), kThreads, 0, s, a, list,
-                                p.prompt_grid, p.tiles, p.prompt_target, min_rows))
-    return st;
-  if (int st = launch_dependent(paged_prompt_kernel, dim3(static_cast<unsigned>(p.prompt_grid)),
-                                kThreads, kSmemBytes, s, a, static_cast<const PromptUnit*>(list)))
-    return st;
-  if (!p.prompt_combine) return QOQ_OK;
-  const long long ctas = static_cast<long long>(p.tiles) * a.Hkv * (kSlotRows / kCombineRows);
-  return launch_dependent(paged_prompt_combine_kernel, dim3(static_cast<unsigned>(ctas)), 256, 0, s,
-                          a, min_rows);
+  return launch_dependent(paged_prompt_kernel, dim3(static_cast<unsigned>(p.prompt_grid)), kThreads,
+                          kSmemBytes, s, a, units);
 }
 
 int prompt_device_error(unsigned int* value, int clear) {
