@@ -57,6 +57,7 @@ constexpr int kStageBytes = 2 * kBlockBytes;         // an iteration is two bloc
 constexpr int kMinBlocks = 16;                       // a run's least length
 constexpr int kPairCost = 12;                        // a pair's beginning and end, in blocks
 constexpr float kRaise = 2.9f;
+constexpr float kHeadroom = 2.0f;
 constexpr float kFixed = 32512.0f;                   // 127 * 256: a query row's largest value
 
 // CTAs of the decode kernel on an SM, by its tiles of four rows.
@@ -392,7 +393,8 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            top = fmaxf(top, mrun[nt]);
+            // (kHeadroom above the score: most rows then need no second raise)
+            top = top > mrun[nt] ? top + kHeadroom : mrun[nt];
             const float al = top == -INFINITY ? 1.0f : fast_exp2(mrun[nt] - top);
             mrun[nt] = top;
             lsum[nt] *= al;
