@@ -479,8 +479,10 @@ QOQ_API int qoq_kv4_decode_attention(const void* Q, const uint8_t* k_codes, cons
  *           q_start[B] belong to no sequence and their outputs are left as they
  *           were (padded batches).  All of these are device arrays, read by the
  *           kernels: a captured graph follows their contents.
- *   limits  width * page < 2^31 tokens, pages * Hkv * page / 16 < 2^31 blocks,
- *           Hq, Hkv <= 65535 (QOQ_ERR_UNSUPPORTED past them).
+ *   limits  width * page <= 2^31 - 4096 tokens, pages * Hkv * page / 16 < 2^31
+ *           blocks, Hq, Hkv <= 65535; for attention also (width * page / 16 + 13)
+ *           times Hkv < 2^31 and times B < 2^40, B * Hkv <= 2^22 and T * Hq <= 2^30
+ *           (QOQ_ERR_UNSUPPORTED past them).
  * T = 0 and B = 0 are calls with nothing to do.
  * ---------------------------------------------------------------------- */
 QOQ_API int qoq_kv4_paged_bytes(int pages, int Hkv, int page, int d, size_t* k_bytes,

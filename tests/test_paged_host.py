@@ -230,6 +230,19 @@ def test_attention_refusals(L):
     assert _attend(L, B=0, ws=None, ws_bytes=0) == qoq.QOQ_OK
 
 
+def test_attention_refuses_what_its_block_counts_cannot_hold(L):
+    """A table may name a page many times: more blocks than the pool has."""
+    UNS = qoq.QOQ_ERR_UNSUPPORTED
+    for bad in (dict(width=1 << 22, page=256, Hq=32, Hkv=32, ldq=32 * 128),   # 2^31 blocks and more
+                dict(width=1 << 22, page=256, B=1 << 14),                     # 2^40 in the batch
+                dict(width=(1 << 27) - 1)):                                   # tokens up to 2^31 - 16
+        assert _attend(L, **bad) == UNS, bad
+    assert _append(L, width=(1 << 27) - 1) == UNS
+    f = L.qoq_kv4_paged_attention_workspace_bytes
+    assert f(4, 32, 32, 128, 2, 1 << 22, 256, 1) == 0
+    assert f(4, 4, 1, 128, 2, 1 << 22, 256, 1) > 0
+
+
 def test_workspace_is_bounded_and_zero_for_nothing(L):
     f = L.qoq_kv4_paged_attention_workspace_bytes
     assert f(0, 4, 1, 128, 2, 64, 16, 1) == 0

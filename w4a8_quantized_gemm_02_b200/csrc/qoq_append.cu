@@ -482,7 +482,8 @@ int check_paged_shape(int pages, int Hkv, int page, int d) {
 
 int check_batch(int T, int B, int width, int page) {
   if (T < 0 || B < 0 || width <= 0) return QOQ_ERR_INVALID_ARG;
-  if (width > 0x7fffffff / page) return QOQ_ERR_UNSUPPORTED;   // positions are 32-bit
+  // tokens are 32-bit numbers, also those of a tile that begins at a sequence's last one
+  if (width > (0x7fffffff - 4095) / page) return QOQ_ERR_UNSUPPORTED;
   return QOQ_OK;
 }
 

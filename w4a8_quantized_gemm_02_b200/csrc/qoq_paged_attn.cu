@@ -732,6 +732,10 @@ int check_paged_attention(int T, int Hq, int Hkv, int d, int B, int width, int p
   // numbers of work units and of rows are 32-bit
   if (static_cast<long long>(B) * Hkv > (1 << 22) || static_cast<long long>(T) * Hq > (1LL << 30))
     return QOQ_ERR_UNSUPPORTED;
+  // a sequence's place among its KV heads' blocks is 32-bit, the batch's sum of blocks has
+  // 40 bits (a table may name a page many times, so the pool's size bounds neither)
+  const long long blocks = static_cast<long long>(width) * (page / 16) + kPairCost + 1;
+  if (blocks * Hkv > 0x7fffffffLL || blocks * B > (1LL << 40) - 1) return QOQ_ERR_UNSUPPORTED;
   return QOQ_OK;
 }
 
