@@ -12,7 +12,6 @@ raised.
 from __future__ import annotations
 
 import ctypes
-import functools
 import math
 import os
 import threading
@@ -487,49 +486,37 @@ def _on(t, stream):
     return stack
 
 
-_torch = None
+_calls = None
 
 
-def _load_torch():
-    """torch, imported at the first call that needs it."""
-    global _torch
-    import torch
-    _torch = torch
-    return torch
+def _load_calls():
+    """The extension that makes calls whose arguments are all as the kernels take
+    them, on the current device and stream, in a tenth of the time; it returns
+    None for any other."""
+    global _calls
+    import torch  # noqa: F401  (its libraries come first)
+    try:
+        from . import _torch_calls
+    except ImportError as e:
+        raise RuntimeError(f"the extension _torch_calls has not been built: {e}") from e
+    _calls = _torch_calls
+    return _calls
 
 
 def _elsewhere(t, stream):
     """Whether a call on `t` is not simply one on the current device's current
     stream.  Such a call is made again inside _on, so that its outputs and
     workspace belong to the stream it runs on."""
-    return stream is not None or t.get_device() != _torch.cuda.current_device()
-
-
-def _current_stream(device: int) -> int:
-    """The address of a device's current stream."""
-    try:
-        return _torch._C._cuda_getCurrentRawStream(device)
-    except AttributeError:   # the public way, which takes 20 times as long
-        return _torch.cuda.current_stream(device).cuda_stream
-
-
-def _need(t, name, dtype, shape, dev):
-    """_need_cuda of a dtype, shape and CUDA device, quick for a tensor that has
-    them: these calls take a few microseconds on the device."""
-    try:
-        if t.dtype is dtype and t.shape == shape and t.device == dev and t.is_contiguous():
-            return
-    except AttributeError:
-        pass
-    _need_cuda(t, name, dtype, shape=shape, device=dev)
+    import torch
+    return stream is not None or t.get_device() != torch.cuda.current_device()
 
 
 def _need_rows(t, name, dtype, width, device=None):
     """A CUDA tensor of rows of `width` contiguous elements, the rows any
     multiple of 16 bytes apart; returns (rows, elements between rows)."""
-    torch = _torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() == 0:
+        raise ValueError(f"{name} must be a CUDA tensor of rows")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
@@ -552,23 +539,23 @@ def _need_rows(t, name, dtype, width, device=None):
 
 def _need_batch(cache, q_start, seqlen, block_table, dev):
     """Checks a paged cache and a ragged batch; returns (pages, Hkv, page, B, width)."""
-    torch = _torch
+    import torch
     kc, vc, sc = cache
     shape = getattr(sc, "shape", ())
     if len(shape) != 4 or shape[3] != 4 or shape[2] % 16:
         raise ValueError("scales must have shape (pages, Hkv, page, 4), page a multiple of 16")
     pages, Hkv, page, _ = shape
-    _need(sc, "scales", torch.float16, shape, dev)
+    _need_cuda(sc, "scales", torch.float16, shape=shape, device=dev)
     shape = (pages, Hkv, page // 16, 1024)
-    _need(kc, "k_codes", torch.uint8, shape, dev)
-    _need(vc, "v_codes", torch.uint8, shape, dev)
+    _need_cuda(kc, "k_codes", torch.uint8, shape=shape, device=dev)
+    _need_cuda(vc, "v_codes", torch.uint8, shape=shape, device=dev)
     shape = getattr(block_table, "shape", ())
     if len(shape) != 2:
         raise ValueError("block_table must have 2 dims")
     B, width = shape
-    _need(block_table, "block_table", torch.int32, shape, dev)
-    _need(seqlen, "seqlen", torch.int32, (B,), dev)
-    _need(q_start, "q_start", torch.int32, (B + 1,), dev)
+    _need_cuda(block_table, "block_table", torch.int32, shape=shape, device=dev)
+    _need_cuda(seqlen, "seqlen", torch.int32, shape=(B,), device=dev)
+    _need_cuda(q_start, "q_start", torch.int32, shape=(B + 1,), device=dev)
     return pages, Hkv, page, B, width
 
 
@@ -674,9 +661,15 @@ def kv4_paged_append(qkv, cache, q_start, seqlen, block_table, Hq: int, inv_freq
     int32.  inv_freq: float64 (rot / 2) from rope_frequencies (None: no
     rotation), rope_layout "half" or "interleaved".  values: (K, V), each
     (T, Hkv, 128) float16, written with the values that the cache then holds."""
-    torch = _torch or _load_torch()
     if rope_layout not in _ROPE_LAYOUTS:
         raise ValueError(f"rope_layout must be one of {sorted(_ROPE_LAYOUTS)}")
+    if stream is None:
+        q = (_calls or _load_calls()).paged_append(
+            qkv, cache, q_start, seqlen, block_table, Hq, inv_freq, _ROPE_LAYOUTS[rope_layout],
+            rope_factor, q_out, values)
+        if q is not None:
+            return q
+    import torch
     if not isinstance(qkv, torch.Tensor) or not qkv.is_cuda:
         raise ValueError("qkv must be a CUDA tensor")
     if _elsewhere(qkv, stream):
@@ -692,18 +685,18 @@ def kv4_paged_append(qkv, cache, q_start, seqlen, block_table, Hq: int, inv_freq
         rot, freq = 2 * inv_freq.shape[0], inv_freq.data_ptr()
     if values is not None:
         kh, vh = values
-        _need(kh, "values[0]", torch.float16, (T, Hkv, 128), dev)
-        _need(vh, "values[1]", torch.float16, (T, Hkv, 128), dev)
+        _need_cuda(kh, "values[0]", torch.float16, shape=(T, Hkv, 128), device=dev)
+        _need_cuda(vh, "values[1]", torch.float16, shape=(T, Hkv, 128), device=dev)
         k_at, v_at = kh.data_ptr(), vh.data_ptr()
     if q_out is None:
         q_out = qkv.new_empty((T, Hq, 128))
     else:
-        _need(q_out, "q_out", torch.float16, (T, Hq, 128), dev)
+        _need_cuda(q_out, "q_out", torch.float16, shape=(T, Hq, 128), device=dev)
     st = lib().qoq_kv4_paged_append(
         qkv.data_ptr(), ld, T, Hq, Hkv, 128, q_start.data_ptr(), seqlen.data_ptr(), B,
         block_table.data_ptr(), width, pages, page, freq, rot, _ROPE_LAYOUTS[rope_layout],
         rope_factor, q_out.data_ptr(), cache[0].data_ptr(), cache[1].data_ptr(),
-        cache[2].data_ptr(), k_at, v_at, _current_stream(dev.index))
+        cache[2].data_ptr(), k_at, v_at, torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _check(st, "qoq_kv4_paged_append")
     return q_out
@@ -718,7 +711,13 @@ def kv4_paged_attention(Q, cache, q_start, seqlen, block_table, max_q=None, scal
     number of rows of a sequence (1 for a decode step; default: T).  scale:
     default 1 / sqrt(128).  ws: a uint8 workspace of
     kv4_paged_attention_workspace_bytes (default: allocated for the call)."""
-    torch = _torch or _load_torch()
+    scale = _DEFAULT_SCALE if scale is None else scale
+    if stream is None:
+        o = (_calls or _load_calls()).paged_attention(Q, cache, q_start, seqlen, block_table,
+                                                      max_q, scale, out, ws)
+        if o is not None:
+            return o
+    import torch
     if not isinstance(Q, torch.Tensor) or Q.dim() != 3 or Q.shape[2] != 128:
         raise ValueError("Q must have shape (T, Hq, 128)")
     if not Q.is_cuda:
@@ -731,35 +730,23 @@ def kv4_paged_attention(Q, cache, q_start, seqlen, block_table, max_q=None, scal
     T, ldq = _need_rows(Q, "Q", torch.float16, Hq * 128)
     pages, Hkv, page, B, width = _need_batch(cache, q_start, seqlen, block_table, dev)
     max_q = max(T, 1) if max_q is None else max_q
-    scale = _DEFAULT_SCALE if scale is None else scale
     if out is None:
         out = Q.new_empty((T, Hq, 128))
     else:
-        _need(out, "out", torch.float16, (T, Hq, 128), dev)
+        _need_cuda(out, "out", torch.float16, shape=(T, Hq, 128), device=dev)
     if ws is None:
-        ws = cache[0].new_empty(_attention_ws(dev.index, T, Hq, Hkv, B, width, page, max_q))
+        ws = cache[0].new_empty(kv4_paged_attention_workspace_bytes(T, Hq, Hkv, B, width, page,
+                                                                    max_q))
     else:
         _need_ws(ws, dev)
     st = lib().qoq_kv4_paged_attention(
         Q.data_ptr(), ldq, T, Hq, Hkv, 128, cache[0].data_ptr(), cache[1].data_ptr(),
         cache[2].data_ptr(), q_start.data_ptr(), seqlen.data_ptr(), B, block_table.data_ptr(),
         width, pages, page, max_q, scale, out.data_ptr(), ws.data_ptr(), ws.numel(),
-        _current_stream(dev.index))
+        torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _check(st, "qoq_kv4_paged_attention")
     return out
-
-
-@functools.lru_cache(maxsize=256)
-def _attention_ws(device, T, Hq, Hkv, B, width, page, max_q):
-    """kv4_paged_attention_workspace_bytes on the current device (its number is
-    only a key: the size depends on the SM count)."""
-    return kv4_paged_attention_workspace_bytes(T, Hq, Hkv, B, width, page, max_q)
-
-
-@functools.lru_cache(maxsize=256)
-def _lora_ws(device, T, K, N, R, n):
-    return lora_workspace_bytes(T, K, N, R, n)
 
 
 def kv4_paged_attention_workspace_bytes(T: int, Hq: int, Hkv: int, B: int, width: int, page: int,
@@ -954,7 +941,11 @@ def lora_add(Y, X, A, B, ids, scaling, out=None, ws=None, stream=None):
     Y (T, N), X (T, K), A (n, R, K), B (n, N, R) float16, ids (T,) int32,
     scaling (n,) float32.  out: a (T, N) float16 tensor, which may be Y
     (default: a new one)."""
-    torch = _torch or _load_torch()
+    if stream is None:
+        o = (_calls or _load_calls()).lora_add(Y, X, A, B, ids, scaling, out, ws)
+        if o is not None:
+            return o
+    import torch
     if not isinstance(X, torch.Tensor) or not X.is_cuda or X.dim() != 2:
         raise ValueError("X must be a CUDA tensor with 2 dims")
     if _elsewhere(X, stream):
@@ -965,23 +956,23 @@ def lora_add(Y, X, A, B, ids, scaling, out=None, ws=None, stream=None):
     if len(shape) != 3:
         raise ValueError("B must have 3 dims")
     n, N, R = shape
-    _need(X, "X", torch.float16, (T, K), dev)
-    _need(Y, "Y", torch.float16, (T, N), dev)
-    _need(A, "A", torch.float16, (n, R, K), dev)
-    _need(B, "B", torch.float16, shape, dev)
-    _need(ids, "ids", torch.int32, (T,), dev)
-    _need(scaling, "scaling", torch.float32, (n,), dev)
+    _need_cuda(X, "X", torch.float16, shape=(T, K), device=dev)
+    _need_cuda(Y, "Y", torch.float16, shape=(T, N), device=dev)
+    _need_cuda(A, "A", torch.float16, shape=(n, R, K), device=dev)
+    _need_cuda(B, "B", torch.float16, shape=shape, device=dev)
+    _need_cuda(ids, "ids", torch.int32, shape=(T,), device=dev)
+    _need_cuda(scaling, "scaling", torch.float32, shape=(n,), device=dev)
     if out is None:
         out = torch.empty_like(Y)
     elif out is not Y:
-        _need(out, "out", torch.float16, (T, N), dev)
+        _need_cuda(out, "out", torch.float16, shape=(T, N), device=dev)
     if ws is None:
-        ws = torch.empty(_lora_ws(dev.index, T, K, N, R, n), dtype=torch.uint8, device=dev)
+        ws = torch.empty(lora_workspace_bytes(T, K, N, R, n), dtype=torch.uint8, device=dev)
     else:
         _need_ws(ws, dev)
     st = lib().qoq_lora_add(Y.data_ptr(), X.data_ptr(), T, K, N, A.data_ptr(), B.data_ptr(), R, n,
                             ids.data_ptr(), scaling.data_ptr(), out.data_ptr(), ws.data_ptr(),
-                            ws.numel(), _current_stream(dev.index))
+                            ws.numel(), torch.cuda.current_stream(dev).cuda_stream)
     if st:
         _check(st, "qoq_lora_add")
     return out

@@ -1,4 +1,5 @@
-"""Build ``libqoq.so`` (the CUDA library) in-tree with nvcc for sm_100a.
+"""Build ``libqoq.so`` (the CUDA library) in-tree with nvcc for sm_100a, and
+``_torch_calls.so`` (the calls from torch tensors into it) with g++.
 
     python -m w4a8_quantized_gemm_02_b200.build [--force]
 """
@@ -15,6 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqoq.so")
+CALLS = os.path.join(PKG, "_torch_calls.so")
+CALLS_SRC = os.path.join(CSRC, "qoq_torch.cpp")
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -44,8 +47,34 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def build_calls(force: bool = False, verbose: bool = False) -> str:
+    """The extension module, against the installed torch's headers."""
+    import importlib.util
+    import sysconfig
+    deps = (CALLS_SRC, os.path.join(INCLUDE, "qoq.h"))
+    if (not force and os.path.exists(CALLS)
+            and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in deps)):
+        return CALLS
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = CALLS + f".tmp{os.getpid()}"
+    # torch's libraries are in the process already (torch is imported first); libqoq.so lies
+    # beside the module
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-I", INCLUDE,
+           "-I", os.path.join(torch, "include"), "-I", os.path.join(cuda, "include"),
+           "-I", sysconfig.get_paths()["include"], CALLS_SRC, "-o", tmp,
+           "-L", PKG, "-L", os.path.join(torch, "lib"), "-l:libqoq.so", "-ltorch_python",
+           "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    subprocess.check_call(cmd)
+    os.replace(tmp, CALLS)
+    return CALLS
+
+
 def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and not _stale():
+        build_calls(verbose=verbose)
         return LIB
     objdir = os.path.join(PKG, "_build")
     os.makedirs(objdir, exist_ok=True)
@@ -64,6 +93,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
     os.replace(tmp, LIB)
+    build_calls(force, verbose)
     return LIB
 
 
