@@ -13,7 +13,8 @@
 // touches as small as v^ about its vector's middle.
 //
 // Warps.  Warpgroups 0 and 1 do the softmax of one tile each; warpgroup 2 turns codes
-// into FP16 tiles; one thread of warpgroup 3 issues the MMAs of whichever tile is ready.
+// into FP16 tiles; a thread of warpgroup 3 for each tile issues its MMAs (one thread for
+// both had no time left: an issue takes it some 55 cycles, a commit 200).
 // Tensor memory (512 columns) holds S and O of both tiles; W overwrites the scores it
 // came from.  A step's softmax goes by halves of 64 tokens, so that O += W V of the
 // first half runs beside the second half's softmax, and one tile's products beside the
@@ -66,8 +67,8 @@ constexpr uint32_t kSmemBytes = kV + 4 * kHalf + 1024;   // + alignment
 
 struct Bars {
   uint64_t q_full, k_full[2], k_empty[2], v_full[2], v_empty[2], c_full[2];
-  uint64_t s_full[2], p_full[2][2];        // [tile], [tile][half step]
-  uint64_t o_done[2], o_full;
+  uint64_t s_full[2][2], p_full[2][2];     // [tile][half step]
+  uint64_t o_full;
 };
 
 __device__ __forceinline__ void mma_f16_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
@@ -303,13 +304,14 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
       mbar_init(bar(bars.k_full[i]), 4);
       mbar_init(bar(bars.v_full[i]), 4);
       mbar_init(bar(bars.c_full[i]), 4);
-      mbar_init(bar(bars.k_empty[i]), 1);
-      mbar_init(bar(bars.v_empty[i]), 1);
-      mbar_init(bar(bars.o_done[i]), 1);
-      mbar_init(bar(bars.s_full[i]), 1);
-      for (int h = 0; h < 2; ++h) mbar_init(bar(bars.p_full[i][h]), 4);
+      mbar_init(bar(bars.k_empty[i]), two ? 2 : 1);
+      mbar_init(bar(bars.v_empty[i]), two ? 2 : 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(bar(bars.s_full[i][h]), 1);
+        mbar_init(bar(bars.p_full[i][h]), 4);
+      }
     }
-    mbar_init(bar(bars.o_full), 1);
+    mbar_init(bar(bars.o_full), two ? 2 : 1);
     fence_mbar_init();
   }
   if (warp == 12) {
@@ -400,11 +402,11 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
       uint32_t absent2 = 0;
       for (int hs = 0; hs < 2 * steps; ++hs) {
         const int j = hs >> 1, hf = hs & 1;
+        ok = wait(bars.s_full[x][hf], j & 1, kErrEpilogue) &&
+             (hf == 1 || wait(bars.c_full[j & 1], (j >> 1) & 1, kErrEpilogue));
+        if (!ok) break;
+        tc_fence_after_sync();
         if (hf == 0) {
-          ok = wait(bars.s_full[x], j & 1, kErrEpilogue) &&
-               wait(bars.c_full[j & 1], (j >> 1) & 1, kErrEpilogue);
-          if (!ok) break;
-          tc_fence_after_sync();
           absent2 = s_absent[j & 1][0] | s_absent[j & 1][1] | s_absent[j & 1][2] | s_absent[j & 1][3];
         }
         const uint32_t t_h = t_s + (kTile / 2) * hf;
@@ -479,8 +481,9 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
             for (int k = 0; k < 8; ++k) s[i][k] = add2(s[i][k], d2);
           }
           if (hs > 0) {
-            // the last product into O (for a first half the scores came after it)
-            ok = wait(bars.o_done[x], (hs - 1) & 1, kErrEpilogue);
+            // the last product into O: announced with the scores issued behind it (the one
+            // before it came ahead of the scores here)
+            ok = wait(bars.s_full[x][1 - hf], (j + hf) & 1, kErrEpilogue);
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll
@@ -697,81 +700,60 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
     }
   } else {
     regs_dec<80>();
-    if (warp == 12 && lane == 0 && steps > 0) {
+    const uint32_t x = warp - 12;          // the tile
+    if (lane == 0 && steps > 0 && (x == 0 || (x == 1 && two))) {
       // ------------------------------------------------------------------ MMA
-      const uint32_t tiles_here = two ? 2 : 1;
-      auto spin = [&](uint64_t& x, uint32_t parity, uint32_t err) {
-        return spin_wait(smem_u32(&x), parity, &s_abort, err);
+      auto spin = [&](uint64_t& b, uint32_t parity) {
+        return spin_wait(smem_u32(&b), parity, &s_abort, kErrMma);
       };
       // (descriptors differ in their low word only: an address in units of 16 bytes)
-      const uint64_t dq = smem_desc_sw128(s0 + kQ), dk = smem_desc_sw128(s0 + kK);
-      const uint64_t dv = smem_desc_sw128(s0 + kV);
-      auto scores = [&](uint32_t x, int st) {
+      const uint64_t dq = smem_desc_sw128(s0 + kQ + x * 2 * kHalf);
+      const uint64_t dk = smem_desc_sw128(s0 + kK), dv = smem_desc_sw128(s0 + kV);
+      const uint32_t t_s = tmem + kTile * x, t_o = t_s + 2 * kTile;
+      // scores of half a step: 64 rows of the K tile
+      auto scores = [&](int st, int hf) {
 #pragma unroll
         for (int ks = 0; ks < 8; ++ks) {
           const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-          mma_f16_ss(tmem + kTile * x, dq + ((x * 2 * kHalf) >> 4) + at,
-                     dk + ((st * 2 * kHalf) >> 4) + at, idesc_f16(kTile), ks > 0);
+          mma_f16_ss(t_s + (kTile / 2) * hf, dq + at,
+                     dk + ((st * 2 * kHalf + hf * (kHalf / 2)) >> 4) + at, idesc_f16(kTile / 2),
+                     ks > 0);
         }
-        mma_commit(bar(bars.s_full[x]));
       };
-      bool ok = spin(bars.q_full, 0, kErrMma) && spin(bars.k_full[0], 0, kErrMma);
+      bool ok = spin(bars.q_full, 0) && spin(bars.k_full[0], 0);
       if (ok) {
         tc_fence_after_sync();
-        for (uint32_t x = 0; x < tiles_here; ++x) scores(x, 0);
+        for (int h = 0; h < 2; ++h) {
+          scores(0, h);
+          mma_commit(bar(bars.s_full[x][h]));
+        }
         mma_commit(bar(bars.k_empty[0]));
       }
-      // per tile the next half step; a stage is free when both tiles have passed it
-      int at[2] = {0, two ? 0 : 2 * steps};
-      int k_ready = 0, v_ready = -1;          // steps whose K and V have arrived
-      long long since = sm_clock();
-      for (int polls = 0; ok && (at[0] < 2 * steps || at[1] < 2 * steps); ++polls) {
+      for (int hs = 0; ok && hs < 2 * steps; ++hs) {
+        const int j = hs >> 1, hf = hs & 1, st = j & 1, next = st ^ 1;
+        ok = spin(bars.p_full[x][hf], j & 1) && (hf == 1 || spin(bars.v_full[st], (j >> 1) & 1));
+        if (!ok) break;
+        tc_fence_after_sync();
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int hs = at[x], j = hs >> 1, hf = hs & 1, st = j & 1, next = (j + 1) & 1;
-          if (hs >= 2 * steps || !mbar_test(bar(bars.p_full[x][hf]), j & 1)) continue;
-          if (v_ready < j) {
-            ok = spin(bars.v_full[st], (j >> 1) & 1, kErrMma);
+        for (int ks = 0; ks < 4; ++ks)
+          mma_f16_ts(t_o, t_s + (kTile / 2) * hf + 8 * ks,
+                     dv + ((st * 2 * kHalf + hf * kHalf + ks * 32) >> 4), idesc_f16(kTile),
+                     hs > 0 || ks > 0);
+        if (hf == 1) mma_commit(bar(bars.v_empty[st]));
+        if (j + 1 < steps) {
+          // the same half of the next step's scores, over the weights just multiplied: they
+          // are there when the softmax of the other half is done
+          if (hf == 0) {
+            ok = spin(bars.k_full[next], ((j + 1) >> 1) & 1);
             if (!ok) break;
-            v_ready = j;
+            tc_fence_after_sync();
           }
-          tc_fence_after_sync();
-#pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            mma_f16_ts(tmem + 2 * kTile + kTile * x, tmem + kTile * x + (kTile / 2) * hf + 8 * ks,
-                       dv + ((st * 2 * kHalf + hf * kHalf + ks * 32) >> 4), idesc_f16(kTile),
-                       hs > 0 || ks > 0);
-          mma_commit(bar(bars.o_done[x]));
-          at[x] = hs + 1;
-          if (hf == 1) {
-            const bool both = at[1 - x] > hs;      // the other tile is done with the step
-            if (both) mma_commit(bar(bars.v_empty[st]));
-            if (j + 1 < steps) {
-              if (k_ready < j + 1) {
-                ok = spin(bars.k_full[next], ((j + 1) >> 1) & 1, kErrMma);
-                if (!ok) break;
-                tc_fence_after_sync();
-                k_ready = j + 1;
-              }
-              scores(x, next);
-              if (both) mma_commit(bar(bars.k_empty[next]));
-            } else if (both) {
-              mma_commit(bar(bars.o_full));
-            }
-          }
-          since = sm_clock();
-          polls = 0;
+          scores(next, hf);
         }
-        if (polls > 256) {
-          polls = 0;
-          if (s_abort) ok = false;
-          if (sm_clock() - since > kWaitLimitCycles) {
-            s_abort = 1u;
-            atomicOr(&g_prompt_error, kErrMma);
-            ok = false;
-          }
-        }
+        mma_commit(bar(bars.s_full[x][hf]));
+        if (hf == 1 && j + 1 < steps) mma_commit(bar(bars.k_empty[next]));
       }
+      if (ok) mma_commit(bar(bars.o_full));
     }
     __syncwarp();
   }
