@@ -233,12 +233,18 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
   return v;
 }
 
-// Nibbles 4 s and 4 s + 16 of a word as FP16 numbers c - 8 (0x6400 | c is
-// 1024 + c).
-__device__ __forceinline__ uint32_t centred(uint32_t word, int s) {
-  const uint32_t n = and_or(word >> s, 0x000f000fu, 0x64006400u);
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&n), __float2half2_rn(1032.0f));
-  return *reinterpret_cast<const uint32_t*>(&h);
+// Nibbles n and n + 4 (counted from the lowest) of a word as FP16 numbers c - 8, n = 0, 1,
+// 2 and 3: 0x6400 | c is 1024 + c, 0x5400 | 16 c is 64 + c, so one shift serves all four.
+__device__ __forceinline__ void centred(uint32_t word, uint32_t (&d)[4]) {
+  auto less = [](uint32_t n, float k) {
+    const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&n), __float2half2_rn(k));
+    return *reinterpret_cast<const uint32_t*>(&h);
+  };
+  const uint32_t high = word >> 8;
+  d[0] = less(and_or(word, 0x000f000fu, 0x64006400u), 1032.0f);
+  d[1] = less(and_or(word, 0x00f000f0u, 0x54005400u), 72.0f);
+  d[2] = less(and_or(high, 0x000f000fu, 0x64006400u), 1032.0f);
+  d[3] = less(and_or(high, 0x00f000f0u, 0x54005400u), 72.0f);
 }
 
 // mbar_wait by tests that never suspend the thread: what these waits hand over is on the
@@ -400,6 +406,9 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
     bool ok = true;
     if (x == 0 || two) {
       uint32_t absent2 = 0;
+      // (unrolled, the half is a constant: 216 -> 209 us at a 4096-token prompt; four times, or the
+      // MMA loop too, is slower)
+#pragma unroll 2
       for (int hs = 0; hs < 2 * steps; ++hs) {
         const int j = hs >> 1, hf = hs & 1;
         ok = wait(bars.s_full[x][hf], j & 1, kErrEpilogue) &&
@@ -450,7 +459,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
           }
         }
         float high[4];
-        bool raise = false, up_row[4];
+        bool raise = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           float a0 = -INFINITY, a1 = -INFINITY;
@@ -460,19 +469,20 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
             a1 = max3(a1, s[i][k + 1].f[0], s[i][k + 1].f[1]);
           }
           high[i] = fmaxf(a0, a1);
-          high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 1));
-          high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 2));
-          // raise the reference: past the threshold, or at the first token seen
-          up_row[i] = high[i] > kRaise || (!seen[i] && high[i] > -INFINITY);
-          raise |= up_row[i];
+          // raise the reference: past the threshold, or at the first token seen (a row's four
+          // threads agree on it below, in the few half steps that need it)
+          raise |= high[i] > (seen[i] ? kRaise : -INFINITY);
         }
         if (__any_sync(0xffffffffu, raise)) {
           float al[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const float up = up_row[i] ? high[i] + kHeadroom : 0.0f;
+            high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 1));
+            high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 2));
+            const bool up_row = high[i] > (seen[i] ? kRaise : -INFINITY);
+            const float up = up_row ? high[i] + kHeadroom : 0.0f;
             al[i] = seen[i] ? fast_exp2(-up) : 1.0f;
-            seen[i] |= up_row[i];
+            seen[i] |= up_row;
             const F2 d2 = pair2(-up, -up), al2 = pair2(al[i], al[i]);
             ref2[i] = add2(ref2[i], d2);
             l2[i] = mul2(l2[i], al2);
@@ -648,17 +658,16 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
 #pragma unroll
-        for (int j0 = 0; j0 < 2; ++j0) {
-          const int row = 32 * pw + column_of(16 * i + gid + 8 * j0);
+        for (int k = 0; k < 4; ++k) {
+          const uint4 q4 = k4[i][k >> 1];
+          const int kk = (k & 1) + 2 * ((k >> 1) ^ (tig >> 1));
+          uint32_t c0[4], c1[4];
+          centred((k & 1) ? q4.z : q4.x, c0);
+          centred((k & 1) ? q4.w : q4.y, c1);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint4 q4 = k4[i][k >> 1];
-            const uint32_t w0 = (k & 1) ? q4.z : q4.x, w1 = (k & 1) ? q4.w : q4.y;
-            const int kk = (k & 1) + 2 * ((k >> 1) ^ (tig >> 1));
-            sts16(kt + tile_at(row, 4 * tig + kk),
-                  make_uint4(centred(w0, 4 * j0), centred(w0, 4 * j0 + 8), centred(w1, 4 * j0),
-                             centred(w1, 4 * j0 + 8)));
-          }
+          for (int j0 = 0; j0 < 2; ++j0)
+            sts16(kt + tile_at(32 * pw + column_of(16 * i + gid + 8 * j0), 4 * tig + kk),
+                  make_uint4(c0[j0], c0[j0 + 2], c1[j0], c1[j0 + 2]));
         }
       }
       fence_proxy_async_smem();
@@ -688,11 +697,13 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
         const uint4 a4 = v4[0][w >> 2], b4 = v4[1][w >> 2];
         const uint32_t wa = (w & 3) == 0 ? a4.x : (w & 3) == 1 ? a4.y : (w & 3) == 2 ? a4.z : a4.w;
         const uint32_t wb = (w & 3) == 0 ? b4.x : (w & 3) == 1 ? b4.y : (w & 3) == 2 ? b4.z : b4.w;
+        uint32_t ca[4], cb[4];
+        centred(wa, ca);
+        centred(wb, cb);
 #pragma unroll
         for (int j0 = 0; j0 < 2; ++j0)
           sts16(vt + tile_at(16 * w + gid + 8 * j0, 4 * pw + tig),
-                make_uint4(centred(wa, 4 * j0), centred(wa, 4 * j0 + 8), centred(wb, 4 * j0),
-                           centred(wb, 4 * j0 + 8)));
+                make_uint4(ca[j0], ca[j0 + 2], cb[j0], cb[j0 + 2]));
       }
       fence_proxy_async_smem();
       arrive(bars.v_full[st]);
@@ -704,7 +715,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
     if (lane == 0 && steps > 0 && (x == 0 || (x == 1 && two))) {
       // ------------------------------------------------------------------ MMA
       auto spin = [&](uint64_t& b, uint32_t parity) {
-        return spin_wait(smem_u32(&b), parity, &s_abort, kErrMma);
+        return mbar_wait(smem_u32(&b), parity, &s_abort, &g_prompt_error, kErrMma);
       };
       // (descriptors differ in their low word only: an address in units of 16 bytes)
       const uint64_t dq = smem_desc_sw128(s0 + kQ + x * 2 * kHalf);
