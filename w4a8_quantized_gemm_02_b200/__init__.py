@@ -660,7 +660,8 @@ def kv4_paged_append(qkv, cache, q_start, seqlen, block_table, Hq: int, inv_freq
     q_start[b + 1] - 1, its last tokens of seqlen[b]; block_table (B, width)
     int32.  inv_freq: float64 (rot / 2) from rope_frequencies (None: no
     rotation), rope_layout "half" or "interleaved".  values: (K, V), each
-    (T, Hkv, 128) float16, written with the values that the cache then holds."""
+    (T, Hkv, 128) float16, written with the values that the cache then holds.
+    Rows of no sequence are not written (in a new tensor: they hold anything)."""
     if rope_layout not in _ROPE_LAYOUTS:
         raise ValueError(f"rope_layout must be one of {sorted(_ROPE_LAYOUTS)}")
     if stream is None:
@@ -710,7 +711,9 @@ def kv4_paged_attention(Q, cache, q_start, seqlen, block_table, max_q=None, scal
     The batch as for kv4_paged_append, after the append.  max_q: the largest
     number of rows of a sequence (1 for a decode step; default: T).  scale:
     default 1 / sqrt(128).  ws: a uint8 workspace of
-    kv4_paged_attention_workspace_bytes (default: allocated for the call)."""
+    kv4_paged_attention_workspace_bytes (default: allocated for the call).  Rows
+    of no sequence, and of one with more than max_q, are not written (in a new
+    tensor: they hold anything)."""
     scale = _DEFAULT_SCALE if scale is None else scale
     if stream is None:
         o = (_calls or _load_calls()).paged_attention(Q, cache, q_start, seqlen, block_table,
