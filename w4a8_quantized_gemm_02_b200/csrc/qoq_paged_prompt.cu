@@ -274,6 +274,19 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
   const int seqlen = a.seqlen[u.b], len = clamp_len(seqlen, a.width * a.page);
   const bool two = u.row0 + kTile < R;      // the second tile has rows
   const int steps = u.step1 - u.step0;
+  if (steps <= 0) {
+    // Rows that see no token (never split: a split has a step).  They are written from
+    // here: below, rows leave by way of the memory that held Q, and only the products'
+    // end tells that nobody writes or reads Q any more.
+    const int rows = R - u.row0 < kSlotRows ? R - u.row0 : kSlotRows;
+    for (int i = tid; i < rows * (kHeadDim / 8); i += kThreads) {
+      const int r = u.row0 + i / (kHeadDim / 8), qi = r / g;
+      __half* dst = a.out + (static_cast<size_t>(rr.first + qi) * a.Hq + u.hk * g + (r - qi * g)) *
+                                kHeadDim + 8 * (i & (kHeadDim / 8 - 1));
+      *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+    }
+    return;
+  }
   auto bar = [&](uint64_t& x) { return smem_u32(&x); };
 
   if (tid == 0) {
@@ -522,11 +535,11 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
       }
       __syncwarp();        // (a warp reads the rows it wrote)
       const float l = s_row[0][tid], off = s_row[1][tid], mref = s_row[2][tid];
-      if (steps > 0 && ok) ok = wait(bars.o_full, 0, kErrEpilogue);
+      if (ok) ok = wait(bars.o_full, 0, kErrEpilogue);
       if (ok) {
         tc_fence_after_sync();
         const bool whole = u.whole;
-        // (a row that saw no token has l = 0; its O is zero or was not written)
+        // (a row that saw no token has l = 0)
         const float inv = l == 0.0f ? 0.0f : __frcp_rn(l);
         const int rows0 = u.row0 + kTile * x + 32 * (warp & 3);      // the warp's first row
         const int left = R - rows0 < 32 ? R - rows0 : 32;
@@ -537,11 +550,9 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
 #pragma unroll 1
         for (int c = 0; c < kTile; c += 32) {
           float o[32];
-          if (steps > 0) {
-            tmem_ld32(t_o + c, o);
-            tmem_ld_wait();
-            keep(o);
-          }
+          tmem_ld32(t_o + c, o);
+          tmem_ld_wait();
+          keep(o);
 #pragma unroll
           for (int k = 0; k < 32; k += 8) {
             float v[8];
@@ -622,7 +633,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
         }
       }
     };
-    if (steps > 0) fetch(u.step0);
+    fetch(u.step0);
     for (int j = 0; j < steps; ++j) {
       const int st = j & 1, use = j >> 1;
       if (use > 0 && !wait(bars.k_empty[st], (use - 1) & 1, kErrProducer)) break;
@@ -685,7 +696,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
   } else {
     regs_dec<80>();
     const uint32_t x = warp - 12;          // the tile
-    if (lane == 0 && steps > 0 && (x == 0 || (x == 1 && two))) {
+    if (lane == 0 && (x == 0 || (x == 1 && two))) {
       // ------------------------------------------------------------------ MMA
       auto pass = [&](uint64_t& b, uint32_t parity) {
         return mbar_wait(smem_u32(&b), parity, &s_abort, &g_prompt_error, kErrMma);
