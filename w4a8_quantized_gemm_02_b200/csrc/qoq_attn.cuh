@@ -52,6 +52,22 @@ struct PromptUnit;
 int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, const PromptUnit* units,
                         cudaStream_t s);
 
+// A row's running reference.  Token t has the probability p = 2^(x_t - ref) and enters the
+// product with V as the FP16 weight w = p s_V; sums of p stay in FP32, so the reference is
+// free to keep the weights, not the probabilities, in FP16's range: the largest w of a row
+// is never above 2^kWeightTop, and a reference that is set puts it at 2^kWeightSet.  From
+// there down to 2^-14 weights have all their bits, and what is lost below is 2^-35 of the
+// largest: values may be of any size, and a row may have nearly all its weight on one token
+// and thousands of others 2^-20 below.  (A reference at the largest score lost them: with
+// scales of 0.01 and 32000 tokens 12 powers of two below one, up to 9% of the output.)
+// Probabilities reach 2^(kWeightTop + 24) where s_V is FP16's smallest or 0, far inside FP32.
+constexpr float kWeightTop = 15.9f;      // 61147: FP16 ends at 65504
+constexpr float kWeightSet = 10.0f;      // a rise by 5.9 then needs no new reference
+// log2 of a value scale for that: of 0 and NaN the smallest scale's, of infinity the largest's.
+__device__ __forceinline__ float log2_scale(float s) {
+  return __log2f(fminf(fmaxf(s, 5.9604645e-08f), 65504.0f));
+}
+
 // 4 or 8 outputs times `f`, rounded to FP16.
 __device__ __forceinline__ void store_row4(__half* dst, float4 v, float f) {
   const __half2 o[2] = {__floats2half2_rn(v.x * f, v.y * f), __floats2half2_rn(v.z * f, v.w * f)};

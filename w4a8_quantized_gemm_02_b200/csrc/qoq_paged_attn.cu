@@ -14,14 +14,15 @@
 // and two masks unpack eight codes.  That rounds a query value to 2^-16 of its
 // row's largest, less than its own FP16 rounding for values within 32 times of
 // it; a score moves by about 3e-5 of the size of k^ where |q| stays under 4.
-// Outputs: FP16 MMAs, the weights as a high and a low FP16 column (22 bits), the
-// codes centred on 8, which keeps what the tensor cores' FP32 accumulation
+// Outputs: FP16 MMAs, the weights as a high and a low FP16 column (22 bits from 2^-3
+// up, where the largest of a row is at least 2^10; 2^-25 at the least, which is 2^-35 of
+// it), the codes centred on 8, which keeps what the tensor cores' FP32 accumulation
 // touches as small as v^ about its vector's middle: over 131000 tokens, sums of
 // uncentred codes lost half the output's digits (5.5e-4 of it against 2.6e-4).
 //
-// The running maximum is only raised when a score passes it by 2.9 (in log2
-// units): one vote an iteration instead of a reduction.  2^2.9 = 7.46 times the
-// largest scale of a finite FP16 vector, 131008 / 15, is still an FP16 number.
+// The running reference (qoq_attn.cuh) only moves when a weight could pass FP16's
+// range: one vote an iteration instead of a reduction, on the largest scale of a
+// lane's four tokens; the weights themselves are looked at when that vote is carried.
 //
 // Work.  The batch's blocks of 16 tokens, in the order of sequences, KV heads and
 // tokens, are cut into equal runs, one for each resident CTA, whatever the mix of
@@ -56,8 +57,6 @@ constexpr int kBlockBytes = 1024 + 1024 + 128;       // K codes, V codes, scales
 constexpr int kStageBytes = 2 * kBlockBytes;         // an iteration is two blocks
 constexpr int kMinBlocks = 16;                       // a run's least length
 constexpr int kPairCost = 12;                        // a pair's beginning and end, in blocks
-constexpr float kRaise = 2.9f;
-constexpr float kHeadroom = 2.0f;
 constexpr float kFixed = 32512.0f;                   // 127 * 256: a query row's largest value
 
 // CTAs of the decode kernel on an SM, by its tiles of four rows.
@@ -370,6 +369,8 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
         auto hidden = [&](int i, int r, int nt) {
           return kMasked && ((blk + i) * 16 + gid + 8 * r >= lim[nt] || ((gone >> i) & 1u));
         };
+        const float limit = kWeightTop - log2_scale(fmaxf(fmaxf(svt[0][0], svt[0][1]),
+                                                          fmaxf(svt[1][0], svt[1][1])));
         bool raise = false;
         float x[2][NT][2];
 #pragma unroll
@@ -378,14 +379,19 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              // relative to the running maximum (-inf at first: the sum is then no
-              // number below the threshold)
+              // relative to the reference (-inf at first: the sum is then no number
+              // below the threshold)
               float v = fmaf(skt[i][r] * qf[nt], s[i][nt][r], fmaf(mkt[i][r], qh[nt], -mrun[nt]));
               if (hidden(i, r, nt)) v = -INFINITY;
               x[i][nt][r] = v;
-              raise |= !(v <= kRaise);
+              raise |= !(v <= limit);
             }
         if (__any_sync(0xffffffffu, raise)) {
+          float ls[2][2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) ls[i][r] = log2_scale(svt[i][r]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             float y[2][2];
@@ -396,12 +402,13 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
                 y[i][r] = fmaf(skt[i][r] * qf[nt], s[i][nt][r], mkt[i][r] * qh[nt]);
                 if (hidden(i, r, nt)) y[i][r] = -INFINITY;
               }
-            float top = fmaxf(fmaxf(y[0][0], y[0][1]), fmaxf(y[1][0], y[1][1]));
+            // the largest weight's exponent, and the reference that it asks for
+            float top = fmaxf(fmaxf(y[0][0] + ls[0][0], y[0][1] + ls[0][1]),
+                              fmaxf(y[1][0] + ls[1][0], y[1][1] + ls[1][1]));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            // (kHeadroom above the score: most rows then need no second raise)
-            top = top > mrun[nt] ? top + kHeadroom : mrun[nt];
+            top = top - kWeightTop > mrun[nt] ? top - kWeightSet : mrun[nt];
             const float al = top == -INFINITY ? 1.0f : fast_exp2(mrun[nt] - top);
             mrun[nt] = top;
             lsum[nt] *= al;
@@ -458,7 +465,7 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
     cp_async_wait<0>();
     __syncthreads();   // the ring becomes the merge area
 
-    // per warp and row: max, sum, 128 outputs
+    // per warp and row: reference, sum, 128 outputs
     float* mrg = reinterpret_cast<float*>(smem);     // [warp][kRows][kPartFloats]
     static_assert(sizeof(float) * kRows * kPartFloats <= kStages * kStageBytes, "merge area");
 #pragma unroll

@@ -5,12 +5,14 @@
 // rows r = i g + h of one problem; a CTA takes 256 consecutive ones (a slot) as
 // two tiles of 128, and walks the tokens that they see, 128 at a time:
 //     S = Q (c_K - 8)^T        x_t = s_K S_t + (m_K + 8 s_K) Q_sum
-//     W = fp16(2^(x - max) s_V)  O += W (c_V - 8),  o_off += p (m_V + 8 s_V).
+//     W = fp16(2^(x - ref) s_V)  O += W (c_V - 8),  o_off += p (m_V + 8 s_V).
 // The codes enter both products as c - 8, exact FP16 numbers, so the rounding of
 // W (2^-11 relative) is the only one besides the output's: rounding k^ and v^
 // to FP16 instead would save the two scale products a score and cost two more
 // errors of the output's own size.  Centred codes keep what the rounding of W
-// touches as small as v^ about its vector's middle.
+// touches as small as v^ about its vector's middle.  The reference (qoq_attn.cuh) keeps a
+// row's largest W between 2^10 and 2^15.9; a half step is tested by its largest score and
+// its largest value scale, and only where those could pass 2^15.9 by each token's.
 //
 // Warps.  Warpgroups 0 and 1 do the softmax of one tile each; warpgroup 2 turns codes
 // into FP16 tiles; a thread of warpgroup 3 for each tile issues its MMAs (one thread for
@@ -55,9 +57,6 @@ __device__ unsigned int g_prompt_error = 0;
 
 constexpr int kThreads = 512;
 constexpr int kTile = kStepTokens;              // rows of a tile, tokens of a step
-constexpr float kRaise = 2.9f;                  // 2^2.9 * 131008 / 15 is an FP16 number
-constexpr float kHeadroom = 2.0f;               // a raised reference lies this far above the
-                                                // score: a raise rescales O, and one is enough
 
 // Shared memory: Q 2 tiles x 2 halves of 64 dimensions x [128 rows][128 bytes],
 // K and V twice each, 2 halves x [128][128 bytes] (128-byte swizzle).
@@ -258,6 +257,8 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
   __shared__ uint32_t s_tmem;
   __shared__ volatile uint32_t s_abort;
   __shared__ uint32_t s_absent[2][4];       // per step: bit per 16-token block and producer warp
+  __shared__ float2 s_limit[2][2];          // per half step: what scores of its 2 x 32 tokens may
+                                            // lie above the reference
   // scales of two steps, per column pair: (s_K, s_K', m_K, m_K') and (s_V, s_V', m_V, m_V')
   __shared__ float4 s_scale[2][2][kTile / 2];
   __shared__ float s_row[3][kSlotRows];     // Q sums; then l, offset sum and reference
@@ -429,6 +430,8 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
           for (int i = 0; i < 4; ++i)
             s[i][k] = fma2(s[i][k], pair2(kc.x, kc.y), fma2(q2[i], pair2(kc.z, kc.w), ref2[i]));
         }
+        const float2 lim2 = s_limit[j & 1][hf];
+        const float limit = fminf(lim2.x, lim2.y);
         // tokens that a row does not see, or in no page
         const int seen_here = (u.step0 + j) * kTile + (kTile / 2) * hf;
         const uint32_t absent = (absent2 >> (4 * hf)) & 15u;
@@ -444,7 +447,6 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
             }
           }
         }
-        float high[4];
         bool raise = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -454,19 +456,29 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
             a0 = max3(a0, s[i][k].f[0], s[i][k].f[1]);
             a1 = max3(a1, s[i][k + 1].f[0], s[i][k + 1].f[1]);
           }
-          high[i] = fmaxf(a0, a1);
-          // raise the reference: past the threshold, or at the first token seen (a row's four
+          // raise the reference: past the limit, or at the first token seen (a row's four
           // threads agree on it below, in the few half steps that need it)
-          raise |= high[i] > (seen[i] ? kRaise : -INFINITY);
+          raise |= fmaxf(a0, a1) > (seen[i] ? limit : -INFINITY);
         }
         if (__any_sync(0xffffffffu, raise)) {
+          // the largest weights' exponents
+          float high[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float4 vc = sv[4 * k];
+            const float l0 = log2_scale(vc.x), l1 = log2_scale(vc.y);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) high[i] = max3(high[i], s[i][k].f[0] + l0, s[i][k].f[1] + l1);
+          }
           float al[4];
+          raise = false;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 1));
             high[i] = fmaxf(high[i], __shfl_xor_sync(0xffffffffu, high[i], 2));
-            const bool up_row = high[i] > (seen[i] ? kRaise : -INFINITY);
-            const float up = up_row ? high[i] + kHeadroom : 0.0f;
+            const bool up_row = high[i] > (seen[i] ? kWeightTop : -INFINITY);
+            const float up = up_row ? high[i] - kWeightSet : 0.0f;
+            raise |= up_row;
             al[i] = seen[i] ? fast_exp2(-up) : 1.0f;
             seen[i] |= up_row;
             const F2 d2 = pair2(-up, -up), al2 = pair2(al[i], al[i]);
@@ -476,7 +488,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
 #pragma unroll
             for (int k = 0; k < 8; ++k) s[i][k] = add2(s[i][k], d2);
           }
-          if (hs > 0) {
+          if (hs > 0 && __any_sync(0xffffffffu, raise)) {
             // the last product into O: announced with the scores issued behind it (the one
             // before it came ahead of the scores here)
             ok = wait(bars.s_full[x][1 - hf], (j + hf) & 1, kErrEpilogue);
@@ -669,9 +681,14 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
         float* vs = reinterpret_cast<float*>(&s_scale[st][1][c >> 1]) + (c & 1);
         ks[0] = in ? fk.x * scale2 : 0.0f;
         ks[2] = in ? fmaf(8.0f, fk.x, fk.y) * scale2 : 0.0f;
-        vs[0] = in ? fv.x : 0.0f;
+        const float sv = in ? fv.x : 0.0f;
+        vs[0] = sv;
         vs[2] = in ? fmaf(8.0f, fv.x, fv.y) : 0.0f;
-        if (lane == 0) s_absent[st][pw] = gone;
+        const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sv, 0.0f)));
+        if (lane == 0) {
+          s_absent[st][pw] = gone;
+          reinterpret_cast<float*>(s_limit[st])[pw] = kWeightTop - log2_scale(__uint_as_float(top));
+        }
       }
       arrive(bars.c_full[st]);
       // V tile: row dimension, chunk of tokens 32 pw + 8 tig ..
