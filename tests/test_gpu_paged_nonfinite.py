@@ -1,0 +1,90 @@
+"""Infinities and NaN in the paged cache stay with the rows that see them."""
+import math
+
+import numpy as np
+import pytest
+
+import paged_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+if not torch.cuda.is_available():   # pragma: no cover - CPU container
+    pytest.skip("no CUDA device", allow_module_level=True)
+
+import w4a8_quantized_gemm_02_b200 as qoq  # noqa: E402
+
+D = 128
+
+
+def _dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _case(rng, q, past, page, Hq, Hkv):
+    total = np.add(q, past)
+    need = -(-total // page)
+    pages = int(need.sum()) + 1
+    table = np.full((len(q), int(need.max())), -1, np.int32)
+    order, at = rng.permutation(pages), 0
+    for b, n in enumerate(need):
+        table[b, :n] = order[at:at + n]
+        at += n
+    shape = (pages, Hkv, page // 16, 16, D)
+    kc = ref.pack(rng.integers(0, 16, shape).astype(np.uint8), ref.K_AT)
+    vc = ref.pack(rng.integers(0, 16, shape).astype(np.uint8), ref.V_AT)
+    sc = np.empty((pages, Hkv, page, 4), np.float16)
+    sc[..., 0] = rng.uniform(0.1, 0.5, sc.shape[:3])
+    sc[..., 1] = -rng.uniform(1.0, 4.0, sc.shape[:3])
+    sc[..., 2] = rng.uniform(0.1, 0.4, sc.shape[:3])
+    sc[..., 3] = -rng.uniform(1.0, 3.0, sc.shape[:3])
+    q_start = np.concatenate([[0], np.cumsum(q)]).astype(np.int32)
+    Q = rng.standard_normal((int(q_start[-1]), Hq, D)).astype(np.float16)
+    return Q, kc, vc, sc, q_start, total.astype(np.int32), table
+
+
+def _attend(c, max_q):
+    Q, kc, vc, sc, q_start, seqlen, table = (_dev(a) for a in c)
+    out = qoq.kv4_paged_attention(Q, (kc, vc, sc), q_start, seqlen, table, max_q=max_q)
+    return out.cpu().numpy().astype(np.float64)
+
+
+# (up to 16 rows: the single-token kernel; more: the prompt kernel, whole and split)
+SHAPES = [([5], [90], 2, 1), ([4], [2000], 4, 2), ([70], [0], 4, 1), ([70, 130], [333, 1], 4, 2),
+          ([60], [3000], 4, 1)]
+
+
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("q,past,Hq,Hkv", SHAPES)
+def test_a_token_is_not_seen_by_earlier_rows(q, past, Hq, Hkv, which, bad):
+    """A scale or offset of one query token is no number (its codes are then 0, as the quantizer
+    leaves them): the rows before it are what they are without it, the rows from it on are no
+    numbers either."""
+    rng = np.random.default_rng(sum(q) + which)
+    page = 32
+    case = _case(rng, q, past, page, Hq, Hkv)
+    Q, kc, vc, sc, q_start, seqlen, table = case
+    want, tol = ref.attention(Q, kc, vc, sc, q_start, seqlen, table, 1 / math.sqrt(D))
+    dirty, first = sc.copy(), []
+    ck, cv = ref.unpack(kc, ref.K_AT), ref.unpack(vc, ref.V_AT)
+    for b in range(len(q)):
+        i = q[b] // 2 + 1
+        first.append(i)
+        t = past[b] + i
+        dirty[table[b, t // page], :, t % page, which] = bad
+        for c in (ck, cv):
+            c[table[b, t // page], :, t % page // 16, t % 16] = 0
+    got = _attend((Q, ref.pack(ck, ref.K_AT), ref.pack(cv, ref.V_AT), dirty, q_start, seqlen, table),
+                  max(q))
+    for b in range(len(q)):
+        lo, mid, hi = q_start[b], q_start[b] + first[b], q_start[b + 1]
+        assert np.isfinite(got[lo:mid]).all()
+        assert (np.abs(got[lo:mid] - want[lo:mid]) <= tol[lo:mid]).all()
+        if which in (0, 2) or which == 1 and bad != bad:
+            assert np.isnan(got[mid:hi]).all()            # 0 * inf, or a NaN
+        elif which == 3:
+            assert (~np.isfinite(got[mid:hi])).all()
+        # (an infinite offset of a key makes its score infinite: with a negative one the token
+        # has no weight)
+    assert qoq.device_error() == 0

@@ -35,6 +35,7 @@
 // and a last kernel merges.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <math.h>
 
 #include <atomic>
@@ -259,6 +260,10 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
   __shared__ uint32_t s_absent[2][4];       // per step: bit per 16-token block and producer warp
   __shared__ float2 s_limit[2][2];          // per half step: what scores of its 2 x 32 tokens may
                                             // lie above the reference
+  // The first token so far of each producer warp whose value has a scale or offset that is not
+  // finite.  Such scales count as zero (a hidden token's weight 0 times them would be NaN), and
+  // rows that see the token, which are the ones whose limit lies above it, become NaN at the end.
+  __shared__ int s_odd[4];
   // scales of two steps, per column pair: (s_K, s_K', m_K, m_K') and (s_V, s_V', m_V, m_V')
   __shared__ float4 s_scale[2][2][kTile / 2];
   __shared__ float s_row[3][kSlotRows];     // Q sums; then l, offset sum and reference
@@ -530,6 +535,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
         arrive(bars.p_full[x][hf]);
       }
       // the rows' sums, for the epilogue's row a thread
+      const int odd = min(min(s_odd[0], s_odd[1]), min(s_odd[2], s_odd[3]));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float li = l2[i].f[0] + l2[i].f[1], oi = off2[i].f[0] + off2[i].f[1];
@@ -538,6 +544,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
           li += __shfl_xor_sync(0xffffffffu, li, d);
           oi += __shfl_xor_sync(0xffffffffu, oi, d);
         }
+        if (odd < lim[i]) li = NAN;
         if (t == 0) {
           const int ri = kTile * x + 32 * (warp & 3) + 8 * i + gr;
           s_row[0][ri] = li;
@@ -618,6 +625,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
     uint4 k4[2][2], v4[2][2];
     uint2 s4;
     uint32_t gone = 0;
+    int first_odd = INT_MAX;
     auto fetch = [&](int step) {
       gone = 0;
       s4 = make_uint2(0u, 0u);
@@ -675,18 +683,20 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
         const float2 fk = __half22float2(*reinterpret_cast<const __half2*>(&s4.x));
         const float2 fv = __half22float2(*reinterpret_cast<const __half2*>(&s4.y));
         // (a slot past the length may hold anything: its scales count as zero)
-        const bool in = tok < len;
+        const bool in = tok < len, odd = in && !(isfinite(fv.x) && isfinite(fv.y));
         const int c = 32 * pw + column_of(lane);
         float* ks = reinterpret_cast<float*>(&s_scale[st][0][c >> 1]) + (c & 1);
         float* vs = reinterpret_cast<float*>(&s_scale[st][1][c >> 1]) + (c & 1);
         ks[0] = in ? fk.x * scale2 : 0.0f;
         ks[2] = in ? fmaf(8.0f, fk.x, fk.y) * scale2 : 0.0f;
-        const float sv = in ? fv.x : 0.0f;
+        const float sv = in && !odd ? fv.x : 0.0f;
         vs[0] = sv;
-        vs[2] = in ? fmaf(8.0f, fv.x, fv.y) : 0.0f;
+        vs[2] = in && !odd ? fmaf(8.0f, fv.x, fv.y) : 0.0f;
+        first_odd = min(first_odd, __reduce_min_sync(0xffffffffu, odd ? tok : INT_MAX));
         const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaxf(sv, 0.0f)));
         if (lane == 0) {
           s_absent[st][pw] = gone;
+          s_odd[pw] = first_odd;
           reinterpret_cast<float*>(s_limit[st])[pw] = kWeightTop - log2_scale(__uint_as_float(top));
         }
       }
