@@ -1,4 +1,4 @@
-"""Infinities and NaN in the paged cache stay with the rows that see them."""
+"""Infinities and NaN in the paged cache and in queries stay with the rows that see them."""
 import math
 
 import numpy as np
@@ -88,3 +88,35 @@ def test_a_token_is_not_seen_by_earlier_rows(q, past, Hq, Hkv, which, bad):
         # (an infinite offset of a key makes its score infinite: with a negative one the token
         # has no weight)
     assert qoq.device_error() == 0
+
+
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("q,past,Hq,Hkv", [([1], [3], 4, 1), ([1, 1, 1], [900, 40, 5000], 4, 2),
+                                           ([3], [4000], 4, 1)] + SHAPES)
+def test_queries_that_are_no_numbers(q, past, Hq, Hkv, bad):
+    """The row is NaN (scores inf - inf), the others are what they were."""
+    rng = np.random.default_rng(sum(past) + 1)
+    case = _case(rng, q, past, 16, Hq, Hkv)
+    want, tol = ref.attention(*case, 1 / math.sqrt(D))
+    Q, hit = case[0].copy(), np.zeros(case[0].shape[:2], bool)
+    for r in range(0, Q.shape[0], 3):
+        h = int(rng.integers(0, Hq))
+        Q[r, h, int(rng.integers(0, D))] = bad
+        hit[r, h] = True
+    got = _attend((Q, *case[1:]), max(q))
+    assert np.isnan(got[hit]).all()
+    assert (np.abs(got - want)[~hit] <= np.broadcast_to(tol, want.shape)[~hit]).all()
+
+
+def test_keys_that_are_no_numbers_at_all():
+    """Every key of a sequence is NaN, and of another none."""
+    rng = np.random.default_rng(3)
+    for q in ([1, 1], [40, 50]):
+        case = _case(rng, q, [700, 700], 16, 4, 1)
+        want, tol = ref.attention(*case, 1 / math.sqrt(D))
+        sc = case[3].copy()
+        sc[case[6][0]] = np.nan
+        got = _attend((*case[:3], sc, *case[4:]), max(q))
+        n = q[0]
+        assert np.isnan(got[:n]).all()
+        assert (np.abs(got[n:] - want[n:]) <= tol[n:]).all()

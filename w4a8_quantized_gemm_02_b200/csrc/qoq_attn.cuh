@@ -68,6 +68,13 @@ __device__ __forceinline__ float log2_scale(float s) {
   return __log2f(fminf(fmaxf(s, 5.9604645e-08f), 65504.0f));
 }
 
+// The reference that a partial result with the sum l is merged by: -inf for one without
+// tokens, which is left out, and NaN for one that is NaN, which no merge may leave out (its
+// factor is then NaN; fmaxf passes over it).
+__device__ __forceinline__ float part_reference(float l, float ref) {
+  return l == 0.0f ? -INFINITY : (l != l ? l : ref);
+}
+
 // 4 or 8 outputs times `f`, rounded to FP16.
 __device__ __forceinline__ void store_row4(__half* dst, float4 v, float f) {
   const __half2 o[2] = {__floats2half2_rn(v.x * f, v.y * f), __floats2half2_rn(v.z * f, v.w * f)};

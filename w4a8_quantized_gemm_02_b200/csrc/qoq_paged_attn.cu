@@ -478,7 +478,7 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
       }
       float* row = mrg + (warp * kRows + 4 * nt + tig) * kPartFloats;
       if (gid == 0) {
-        row[0] = mrun[nt];
+        row[0] = part_reference(l, mrun[nt]);
         row[1] = l;
       }
 #pragma unroll
@@ -524,7 +524,7 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
         float* part = a.parts + (static_cast<size_t>(2 * blockIdx.x + (c0 == 0 ? 1 : 0)) * kRows +
                                  r) * kPartFloats;
         if (lane == 0) {
-          part[0] = M;
+          part[0] = part_reference(den, M);
           part[1] = den;
         }
         *reinterpret_cast<float4*>(part + 4 + 4 * lane) = v;

@@ -544,7 +544,9 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
           li += __shfl_xor_sync(0xffffffffu, li, d);
           oi += __shfl_xor_sync(0xffffffffu, oi, d);
         }
-        if (odd < lim[i]) li = NAN;
+        // (a query with an infinity has scores of +-inf or NaN: inf - inf in every softmax, also
+        // where all of them are -inf, which a hidden token's score is as well)
+        if (odd < lim[i] || (lim[i] > 0 && !isfinite(q2[i].f[0]))) li = NAN;
         if (t == 0) {
           const int ri = kTile * x + 32 * (warp & 3) + 8 * i + gr;
           s_row[0][ri] = li;
@@ -604,7 +606,7 @@ paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
           float* part = a.parts + (static_cast<size_t>(u.part) * kSlotRows + kTile * x +
                                    32 * (warp & 3)) * kPartFloats;
           if (lane < left) {
-            part[lane * kPartFloats] = l == 0.0f ? -INFINITY : mref;
+            part[lane * kPartFloats] = part_reference(l, mref);
             part[lane * kPartFloats + 1] = l;
           }
 #pragma unroll 4
