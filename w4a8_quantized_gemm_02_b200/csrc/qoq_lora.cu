@@ -374,7 +374,8 @@ __global__ void __launch_bounds__(kShrinkThreads) lora_shrink_kernel(const LoraA
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       hi[i] = __float2half_rn(h4[i]);
-      lo[i] = __float2half_rn(h4[i] - __half2float(hi[i]));
+      // (an infinite value has no low part: inf - inf would make NaN of it)
+      lo[i] = __float2half_rn(isinf(h4[i]) ? 0.0f : h4[i] - __half2float(hi[i]));
     }
     const int row = unit.rows[r];
     __half* h = a.h + static_cast<size_t>(row) * 2 * Rp;
