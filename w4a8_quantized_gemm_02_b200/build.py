@@ -18,6 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libqoq.so")
 CALLS = os.path.join(PKG, "_torch_calls.so")
 CALLS_SRC = os.path.join(CSRC, "qoq_torch.cpp")
+CALLS_STAMP = os.path.join(PKG, "_build", "_torch_calls.txt")   # what it was built against
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -47,15 +48,35 @@ def _stale() -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _torch_dir() -> str:
+    import importlib.util
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _built_against() -> str:
+    """The installed torch (its version.py: version, commit, CUDA) and this Python: a module
+    built against others has another binary interface."""
+    torch = _torch_dir()
+    with open(os.path.join(torch, "version.py")) as f:
+        return f"{torch}\n{sys.version}\n{f.read()}"
+
+
+def _calls_stale() -> bool:
+    if not (os.path.exists(CALLS) and os.path.exists(CALLS_STAMP)):
+        return True
+    t = os.path.getmtime(CALLS)
+    if any(os.path.getmtime(d) > t for d in (CALLS_SRC, os.path.join(INCLUDE, "qoq.h"))):
+        return True
+    with open(CALLS_STAMP) as f:
+        return f.read() != _built_against()
+
+
 def build_calls(force: bool = False, verbose: bool = False) -> str:
     """The extension module, against the installed torch's headers."""
-    import importlib.util
     import sysconfig
-    deps = (CALLS_SRC, os.path.join(INCLUDE, "qoq.h"))
-    if (not force and os.path.exists(CALLS)
-            and all(os.path.getmtime(d) <= os.path.getmtime(CALLS) for d in deps)):
+    if not force and not _calls_stale():
         return CALLS
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    torch = _torch_dir()
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     tmp = CALLS + f".tmp{os.getpid()}"
     # torch's libraries are in the process already (torch is imported first); libqoq.so lies
@@ -68,7 +89,12 @@ def build_calls(force: bool = False, verbose: bool = False) -> str:
     if verbose:
         print(" ".join(cmd), flush=True)
     subprocess.check_call(cmd)
+    os.makedirs(os.path.dirname(CALLS_STAMP), exist_ok=True)
+    if os.path.exists(CALLS_STAMP):
+        os.remove(CALLS_STAMP)     # (no stamp of one build beside the module of another)
     os.replace(tmp, CALLS)
+    with open(CALLS_STAMP, "w") as f:
+        f.write(_built_against())
     return CALLS
 
 
