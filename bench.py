@@ -879,12 +879,13 @@ def run_ours(args):
                    "parallelism": f"independent replicas x{world}" if world > 1 else "1 gpu",
                    "l2": (f"inputs rotated over {nsets} sets ({nsets * per_set / 2**20:.0f} "
                           f"MiB, > 3x L2 {l2 / 2**20:.0f} MiB); one CUDA graph per step")},
-        "roofline": roofline,
-        "per_m": per_m,
-        "layers": layers,
-        "mlp": mlp,
-        "sweep": sweep,
-        "kv4_attention": kv4,
+        "roofline": short(roofline),
+        # (short: readers of the line keep its last 16 KB or so)
+        "per_m": short(per_m),
+        "layers": {name: columns(short(rows)) for name, rows in layers.items()},
+        "mlp": short(mlp),
+        "sweep": short(sweep),
+        "kv4_attention": short(kv4),
         "clocks": clocks,
         "gpu_launches": 2 * len(ms) * args.steps,
         "timed_region": "fused qoq_w4a8_linear per M (dominant M: quantizer + qoq_w4a8_gemm)",
@@ -897,7 +898,7 @@ def run_ours(args):
     if rank == 0 and world == 1 and not args.no_cpu_baseline:
         line["cpu_baseline"] = cpu_baseline(layer, args.cpu_budget_s)
     if rank == 0:
-        print(json.dumps(line), flush=True)
+        print(json.dumps(line, separators=(",", ":")), flush=True)
     if world > 1:
         import torch.distributed as dist
         dist.destroy_process_group()
@@ -1057,6 +1058,23 @@ def load_traffic(workload, M):
         return d.get(workload, {}).get(str(M))
     except Exception:
         return None
+
+
+def short(v):
+    """A record with its floats to five significant digits."""
+    if isinstance(v, float):
+        return float(f"{v:.5g}")
+    if isinstance(v, dict):
+        return {k: short(x) for k, x in v.items()}
+    if isinstance(v, (list, tuple)):
+        return [short(x) for x in v]
+    return v
+
+
+def columns(rows):
+    """Records of one kind as {key: [the rows' values]} (None where a row has none)."""
+    keys = dict.fromkeys(k for r in rows for k in r)
+    return {k: [r.get(k) for r in rows] for k in keys}
 
 
 def main(argv=None):
