@@ -497,8 +497,10 @@ QOQ_API int qoq_kv4_paged_bytes(int pages, int Hkv, int page, int d, size_t* k_b
  *             it); pair j is the dimensions j and j + rot / 2, or 2j and 2j + 1
  *             with interleaved = 1; rotated values are multiplied by
  *             rope_factor.  rot = 0 (inv_freq may be NULL): no rotation.
- *   q_out     [T][Hq][128] FP16, written: the rotated queries.  Not the memory
- *             of qkv.
+ *   q_out     [T][Hq][128] FP16, written: the rotated queries, rotated in
+ *             binary64 where a call has few rows a sequence (under 16 on average) and in
+ *             binary32 otherwise, then rounded: a query may differ by one FP16 step
+ *             between the two (about once in thousands).  Not the memory of qkv.
  *   cache     Keys, rotated in binary64 and rounded to binary32 and then FP16,
  *             and values are quantized as by qoq_kv4_quantize and written to
  *             their slots.  A position outside [0, width * page) or in no page is
@@ -527,9 +529,18 @@ QOQ_API int qoq_kv4_paged_append(const void* qkv, size_t ld, int T, int Hq, int 
  * kernels, and a sequence with more is left as it was.  ws: at least
  * qoq_kv4_paged_attention_workspace_bytes for the same arguments, 16-byte
  * aligned (no zeroing needed), QOQ_ERR_WORKSPACE otherwise; calls that can run
- * at the same time need different workspaces.  Scores, softmax statistics and
- * sums are FP32.  Results do not depend on what else runs.  Asynchronous on
- * `stream`. */
+ * at the same time need different workspaces.
+ *   precision  Scores, softmax statistics and sums are FP32.  Where a sequence has up to 4,
+ *             8 or 16 rows (query tokens x Hq / Hkv; the single-token kernel) queries enter
+ *             as 16-bit fixed point of their row (2^-16 of its largest value) and weights with
+ *             22 bits; elsewhere (the prompt kernel) queries are exact and weights are rounded
+ *             to FP16 once, at any size of the values: the largest weight of a row lies at
+ *             2^10 or above of FP16's range.
+ *   not finite  A row is NaN if its query is not finite, or a vector that it sees was not when
+ *             it was appended (one with an infinity, or all NaN: its scale is then infinite or
+ *             NaN).  Tokens that a row does not see, slots past the length and other rows'
+ *             queries do not affect it.
+ * Results do not depend on what else runs.  Asynchronous on `stream`. */
 QOQ_API size_t qoq_kv4_paged_attention_workspace_bytes(int T, int Hq, int Hkv, int d, int B,
                                                        int width, int page, int max_q);
 QOQ_API int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq, int Hkv, int d,
@@ -547,7 +558,9 @@ QOQ_API int qoq_kv4_paged_attention(const void* Q, size_t ldq, int T, int Hq, in
  *   X [T][K], Y, out [T][N] FP16 (out may be Y); A [n][R][K], B [n][N][R] FP16;
  *   ids int32 [T] (any order: rows are taken by adapter); scaling FP32
  *   [n].  N % 128 == 0, K % 128 == 0, R % 8 == 0, R <= 128 (adapters of smaller
- *   rank: zeros), n <= 4096, T <= 2^20; T = 0 is a call with nothing to do.
+ *   rank: zeros), n <= 4096, T <= 2^20, and with U = T / 4096 (rounded up) times the
+ *   smaller of T, 4096 and 64 + n + 1, 2 U N / 128 < 2^31 (QOQ_ERR_UNSUPPORTED past
+ *   them); T = 0 is a call with nothing to do.
  *   ws: at least qoq_lora_workspace_bytes, 16-byte aligned (no zeroing needed),
  *   QOQ_ERR_WORKSPACE otherwise; calls that can run at the same time need
  *   different workspaces.

@@ -14,7 +14,10 @@
 // are rotated in binary64.  The angle is reduced in turns: with 1/(2 pi) as a
 // pair of doubles, h + l = inv_freq / (2 pi) to about 2^-100, p h is split by an
 // FMA into its rounded value and the rest, and the fraction of a turn goes to
-// sincospi: the error is about 2^-53 turns for any 32-bit position.
+// sincospi: the error is about 2^-53 turns for any 32-bit position.  Queries cross no
+// such border: their angles are reduced the same way, and in prompts (by blocks) their
+// products are binary32, 2^-21 of the pair's size beside the FP16 rounding; binary64 would
+// take more conversions a pair than it has arithmetic.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

@@ -97,12 +97,12 @@ __device__ __forceinline__ int weight_of(int blocks) {
   return blocks < 0 ? 0 : kPairCost + (blocks == 0 ? 1 : blocks);
 }
 
-// Measured (32 / 8 heads): 64 sequences of 300 - 8100 tokens, 292 MB, 72.8 us with the merge
-// (4.0 TB/s, 62% of the copy rate); two of 120000 - 131000, 265 MB, 63 us; 64 / 64 heads, 24
-// sequences of 1000 - 2047, 310 MB, 78 us.  Issue slots and the integer pipe are half used
+// Measured (32 / 8 heads): 64 sequences of 300 - 8100 tokens, 292 MB, 74 us with the merge
+// (3.9 TB/s, 60% of the copy rate); two of 120000 - 131000, 265 MB, 64 us; 64 / 64 heads, 24
+// sequences of 1000 - 2047, 310 MB, 79 us.  Issue slots and the integer pipe are half used
 // and DRAM a little more: what is left is latency between dependent instructions, at the 16
-// warps an SM that the registers allow.  3 or 4 copy stages and an unrolled loop were no
-// faster.
+// warps an SM that the registers allow, the ring that runs dry at each pair's end, and the
+// merge.  3 or 4 copy stages and an unrolled loop were no faster.
 //
 // Grid: `ctas` CTAs, one for each that is resident, and one more where there may be
 // prompt chunks, which lists their units.

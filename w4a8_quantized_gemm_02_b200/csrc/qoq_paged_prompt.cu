@@ -247,10 +247,11 @@ __device__ __forceinline__ void centred(uint32_t word, uint32_t (&d)[4]) {
   d[3] = less(and_or(high, 0x00f000f0u, 0x54005400u), 72.0f);
 }
 
-// Measured: a 4096-token prompt (32 / 8 heads) 215 us in all, 639 TFLOP/s of the two products
-// over the pairs that the mask leaves; it is bound by the softmax warps, two on a scheduler,
-// whose instructions and latencies take nearly all of a step (the products would take half
-// of it, the exponentials 2/5).
+// Measured: a 4096-token prompt (32 / 8 heads) 221 us in all, 622 TFLOP/s of the two products
+// over the pairs that the mask leaves (215 us where the reference followed the scores alone);
+// it is bound by the softmax warps, two on a scheduler: at 44% of the issue slots it is their
+// chains' latency (read, scale, compare, exponential, pack, store, announce) that two warps do
+// not cover.  The products would take half of a step, the exponentials 2/5.
 __global__ void __launch_bounds__(kThreads, 1)
 paged_prompt_kernel(const PagedArgs a, const PromptUnit* units) {
   extern __shared__ uint8_t raw[];
