@@ -120,3 +120,21 @@ def test_keys_that_are_no_numbers_at_all():
         n = q[0]
         assert np.isnan(got[:n]).all()
         assert (np.abs(got[n:] - want[n:]) <= tol[n:]).all()
+
+
+@pytest.mark.parametrize("which", [2, 3])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("q,past,Hq,Hkv", [([1], [127], 4, 1), ([1], [5000], 8, 2), ([3], [700], 4, 1),
+                                           ([40], [300], 4, 1), ([40], [6000], 4, 1)])
+def test_a_value_with_hardly_any_weight_counts(q, past, Hq, Hkv, bad, which):
+    """The value that is no number stands among tokens 2^-200 below the others, alone in their
+    part of the sums: any weight of it is too much."""
+    rng = np.random.default_rng(9)
+    page = 16
+    Q, kc, vc, sc, q_start, seqlen, table = _case(rng, q, past, page, Hq, Hkv)
+    Q[:] = rng.choice([0.5, 0.25], Q.shape)
+    sc[..., 0], sc[..., 1] = 0.01, 0.0
+    for t in range(32):
+        sc[table[0, t // page], :, t % page, 1] = -200 / (math.log2(math.e) / math.sqrt(D) * 48)
+    sc[table[0, 0], :, 5, which] = bad
+    assert np.isnan(_attend((Q, kc, vc, sc, q_start, seqlen, table), max(q))).all()

@@ -476,6 +476,9 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
         l += __shfl_xor_sync(0xffffffffu, l, d);
         o += __shfl_xor_sync(0xffffffffu, o, d);
       }
+      // (a value that is not finite shows in o, whose finite terms cannot overflow: the row is NaN,
+      // also where another warp's reference would leave this one's sums out)
+      if (!isfinite(o)) l = NAN;
       float* row = mrg + (warp * kRows + 4 * nt + tig) * kPartFloats;
       if (gid == 0) {
         row[0] = part_reference(l, mrun[nt]);
