@@ -2,7 +2,7 @@
 values of any size, with an allowance that follows the values.
 
 Allowance of an output o = sum p v / sum p, with v = s (c - 8) + (m + 8 s) and the averages
-A = sum p s |c - 8| / sum p, F = sum p |m + 8 s| / sum p and V = sum p |v| / sum p over the n
+A = sum p |s (c - 8)| / sum p, F = sum p |m + 8 s| / sum p and V = sum p |v| / sum p over the n
 tokens that the row sees:
 
 * its own rounding to FP16: 2^-11 |o|, at least 2^-25;
@@ -87,7 +87,7 @@ def attention(Q, kc, vc, sc, q_start, seqlen, table, scale):
             den = p.sum(-1, keepdim=True)
             p = p / torch.where(den == 0, 1.0, den)
             o = p @ v
-            A = p @ ((cv - 8).abs() * s[:, 2:3])
+            A = p @ ((cv - 8) * s[:, 2:3]).abs()
             F = p @ (s[:, 3:4] + 8 * s[:, 2:3]).abs()
             V = p @ v.abs()
             count = sees.sum(-1, keepdim=True).double()

@@ -108,3 +108,11 @@ def test_constant_values_only():
     for q, past in (([1], [900]), ([70], [900])):
         _run(rng, q, past, 4, 1, 16, lambda b, t: np.zeros(t), lambda b, t: rng.uniform(-2.0, 2.0, t),
              SPREAD["sink 12"])
+
+
+@pytest.mark.parametrize("q,past,Hq,Hkv", SHAPES)
+def test_negative_scales(q, past, Hq, Hkv):
+    """Scales that no append writes, but a caller's own cache may hold."""
+    rng = np.random.default_rng(sum(past))
+    _run(rng, q, past, Hq, Hkv, 32, lambda b, t: rng.choice([-0.4, -0.3, 0.2], t),
+         lambda b, t: rng.uniform(-1.0, 1.0, t), SPREAD["sink 12"])

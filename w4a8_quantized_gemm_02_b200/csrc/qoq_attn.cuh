@@ -64,9 +64,10 @@ int launch_paged_prompt(const PagedArgs& a, const PagedPlan& p, const PromptUnit
 // Probabilities reach 2^(kWeightTop + 24) where s_V is FP16's smallest or 0, far inside FP32.
 constexpr float kWeightTop = 15.9f;      // 61147: FP16 ends at 65504
 constexpr float kWeightSet = 10.0f;      // a rise by 5.9 then needs no new reference
-// log2 of a value scale for that: of 0 and NaN the smallest scale's, of infinity the largest's.
+// log2 of a value scale's size for that: of 0 and NaN the smallest scale's, of infinity the
+// largest's.  (Scales that append writes are not negative; a caller's own may be.)
 __device__ __forceinline__ float log2_scale(float s) {
-  return __log2f(fminf(fmaxf(s, 5.9604645e-08f), 65504.0f));
+  return __log2f(fminf(fmaxf(fabsf(s), 5.9604645e-08f), 65504.0f));
 }
 
 // The reference that a partial result with the sum l is merged by: -inf for one without

@@ -97,9 +97,10 @@ __device__ __forceinline__ int weight_of(int blocks) {
   return blocks < 0 ? 0 : kPairCost + (blocks == 0 ? 1 : blocks);
 }
 
-// Measured (32 / 8 heads): 64 sequences of 300 - 8100 tokens, 292 MB, 74 us with the merge
-// (3.9 TB/s, 60% of the copy rate); two of 120000 - 131000, 265 MB, 64 us; 64 / 64 heads, 24
-// sequences of 1000 - 2047, 310 MB, 79 us.  Issue slots and the integer pipe are half used
+// Measured (32 / 8 heads; two cards): 64 sequences of 300 - 8100 tokens, 292 MB, 70 to 74 us
+// with the merge (4.2 to 3.9 TB/s, 64 to 60% of the copy rate); two of 120000 - 131000, 265 MB,
+// 61 to 64 us; 64 / 64 heads, 24 sequences of 1000 - 2047, 310 MB, 76 to 79 us.  (A reference
+// that follows the scores alone: 1% less.)  Issue slots and the integer pipe are half used
 // and DRAM a little more: what is left is latency between dependent instructions, at the 16
 // warps an SM that the registers allow, the ring that runs dry at each pair's end, and the
 // merge.  3 or 4 copy stages and an unrolled loop were no faster.
@@ -369,8 +370,9 @@ paged_decode_kernel(const PagedArgs a, int ctas, const PromptPlan pp) {
         auto hidden = [&](int i, int r, int nt) {
           return kMasked && ((blk + i) * 16 + gid + 8 * r >= lim[nt] || ((gone >> i) & 1u));
         };
-        const float limit = kWeightTop - log2_scale(fmaxf(fmaxf(svt[0][0], svt[0][1]),
-                                                          fmaxf(svt[1][0], svt[1][1])));
+        const float limit =
+            kWeightTop - log2_scale(fmaxf(fmaxf(fabsf(svt[0][0]), fabsf(svt[0][1])),
+                                          fmaxf(fabsf(svt[1][0]), fabsf(svt[1][1]))));
         bool raise = false;
         float x[2][NT][2];
 #pragma unroll
